@@ -23,8 +23,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libbsa.so")
 
 BSA_OK, BSA_ERR_INVALID_ARG, BSA_ERR_UNSUPPORTED, BSA_ERR_CUDA = 0, 1, 2, 3
-BSA_DEV_OK, BSA_DEV_BAD_INDEX, BSA_DEV_TIMEOUT, BSA_DEV_BAD_SCORE = 0, 1, 2, 4
-BSA_BF16, BSA_F32 = 0, 1
+BSA_DEV_OK, BSA_DEV_BAD_INDEX, BSA_DEV_TIMEOUT, BSA_DEV_BAD_SCORE, BSA_DEV_NO_PAGES = 0, 1, 2, 4, 8
+BSA_BF16, BSA_F32, BSA_F16 = 0, 1, 2
 BSA_SCORE_MEAN, BSA_SCORE_MEAN_VNORM, BSA_SCORE_MEAN_VLOG, BSA_SCORE_KMINMAX = 0, 1, 2, 3
 BSA_PATH_CUDA_CORES, BSA_PATH_TENSOR_CORES = 0, 1
 SCORE_KINDS = {"mean": BSA_SCORE_MEAN, "vnorm": BSA_SCORE_MEAN_VNORM, "vlog": BSA_SCORE_MEAN_VLOG,
@@ -35,7 +35,10 @@ EXPORTS = ("bsa_score_workspace_bytes", "bsa_score", "bsa_kv_idx_width",
            "bsa_status_string", "bsa_last_error", "bsa_select_noalloc_max_bytes",
            "bsa_select_noalloc", "bsa_selftest_wait", "bsa_decode_list", "bsa_score_ex",
            "bsa_attend_vs_workspace_bytes", "bsa_attend_vs", "bsa_score_select_workspace_bytes",
-           "bsa_score_select", "bsa_score_path", "bsa_attend_path", "bsa_decode_path")
+           "bsa_score_select", "bsa_score_path", "bsa_attend_path", "bsa_decode_path",
+           "bsa_pages_fork", "bsa_pages_resize", "bsa_pages_copy", "bsa_cache_append", "bsa_cache_compact",
+           "bsa_tree_mask", "bsa_attend_paged_workspace_bytes", "bsa_attend_tree", "bsa_attend_pages",
+           "bsa_select_pages_workspace_bytes", "bsa_select_pages")
 
 
 class BsaError(RuntimeError):
@@ -69,6 +72,15 @@ class DecodeParams(ctypes.Structure):
     _fields_ = [("tau", ctypes.c_float), ("phi", ctypes.c_float), ("patience", ctypes.c_int),
                 ("enable", ctypes.c_int), ("n_probe", ctypes.c_int),
                 ("probe_dims", ctypes.POINTER(ctypes.c_int))]
+
+
+class CacheShape(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("page", ctypes.c_int),
+                ("d", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class PageSelectParams(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_int), ("n_first", ctypes.c_int), ("n_last", ctypes.c_int)]
 
 
 _lib = None
@@ -127,6 +139,26 @@ def lib() -> ctypes.CDLL:
         L.bsa_attend_path.restype = ctypes.c_int
         L.bsa_decode_path.argtypes = [dsp]
         L.bsa_decode_path.restype = ctypes.c_int
+        ci, fl, csp = ctypes.c_int, ctypes.c_float, ctypes.POINTER(CacheShape)
+        L.bsa_pages_fork.argtypes = [ci, ci, ci, ci, vp, vp, vp, vp, i32p, vp]
+        L.bsa_pages_resize.argtypes = [ci, ci, ci, ci, vp, vp, vp, vp, vp, vp, i32p, vp]
+        L.bsa_pages_copy.argtypes = [csp, vp, vp, vp, vp, ci, i32p, vp]
+        L.bsa_cache_append.argtypes = [csp, ci, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, i32p, vp]
+        L.bsa_cache_compact.argtypes = [csp, ci, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, i32p, vp]
+        L.bsa_tree_mask.argtypes = [ci, ci, vp, vp, vp, i32p, vp]
+        L.bsa_attend_paged_workspace_bytes.argtypes = [csp, ci, ci, ci, ci]
+        L.bsa_attend_tree.argtypes = [csp, ci, ci, ci, ci, vp, vp, vp, vp, vp, vp, vp, fl, vp, vp, i32p, vp,
+                                      sz, vp]
+        L.bsa_attend_pages.argtypes = [csp, ci, ci, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, ci, fl, vp, vp,
+                                       i32p, vp, sz, vp]
+        L.bsa_select_pages_workspace_bytes.argtypes = [csp, ci, ci, ci, ci]
+        L.bsa_select_pages.argtypes = [csp, ctypes.POINTER(PageSelectParams), ci, ci, ci, ci, vp, vp, vp, vp,
+                                       vp, vp, vp, vp, i32p, vp, sz, vp]
+        for f in ("pages_fork", "pages_resize", "pages_copy", "cache_append", "cache_compact", "tree_mask",
+                  "attend_tree", "attend_pages", "select_pages"):
+            getattr(L, "bsa_" + f).restype = ctypes.c_int
+        for f in ("attend_paged", "select_pages"):
+            getattr(L, "bsa_" + f + "_workspace_bytes").restype = sz
         L.bsa_status_string.argtypes = [ctypes.c_int]
         L.bsa_status_string.restype = ctypes.c_char_p
         L.bsa_last_error.argtypes = []

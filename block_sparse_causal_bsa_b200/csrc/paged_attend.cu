@@ -1,0 +1,640 @@
+// Attention over a paged cache on warp-level tensor-core MMAs: few query rows per KV head
+// (decode, small trees of drafts), or a list of pages per token.
+//
+//   O = sum softmax(scale q.k) v over the positions a token sees
+//
+// The rows of an item (at most RT = 8 or 16) meet every key of a long cache: 4 d RT flops for 4 d
+// bytes of K and V per key, so the kernel is bound by the HBM reads of the cache. What it does about
+// it: one CTA per SM streams its equal share of all key tiles (paged_work.cuh) through a ring of
+// TMA-fed stages that never drains between items, and the MMAs, exponentials and shared-memory
+// reads of a tile are spread over eight warps so that they stay under the time its bytes take.
+//
+// 288 threads:
+//   warp 0     producer: page numbers of the coming tiles in its lanes' registers (one table read
+//              per 8 to 32 tiles), then per tile one TMA box per page and 64-column half, lanes in
+//              parallel. Pages without a visible row are not read. Per stage it leaves the mask of
+//              the tile's rows that are keys of the item.
+//   warps 1-8  two groups of four, taking tiles in turn; a warp owns 16 keys of its tiles and keeps its
+//              own online softmax over them (maximum m, sum l, unnormalised O):
+//                S = K Q^T (A = K rows by ldmatrix, B = Q in registers), P = 2^(S scale log2 e - m),
+//                O^T += V^T P^T (A = V^T by ldmatrix.trans, B = P^T from S by movmatrix)
+//              P goes into the product as two 16-bit terms (value and rounding remainder), so O carries
+//              no rounding of P: the second MMA is free here, the tensor pipe idles anyway. At the end of
+//              a segment the eight states are joined in shared memory.
+// For fp16, weights are scaled by 2^14: fp16's smallest value is 2^-24, and many small weights
+// would be lost below it.
+// Rows that are no keys (the tail of the last page, missing pages) have their S masked and their
+// V rows zeroed in shared memory, and non-finite values of drafted tokens are taken out of the
+// tile and given back only to rows that see them.
+#include <math.h>
+
+#include "paged_work.cuh"
+#include "tc_common.cuh"
+
+namespace bsa {
+
+namespace {
+
+constexpr int kWarps = 8;                       // compute warps
+constexpr int kThreads = 32 * (kWarps + 1);
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the eight compute warps
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kHalf = kTileKeys * 128;          // 64 rows x 128 bytes
+  static constexpr uint32_t kTile = kHalves * kHalf;          // K or V of a tile
+  static constexpr uint32_t kStage = 2 * kTile;
+  static constexpr int kStages = D == 128 ? 6 : 10;
+};
+
+template <int D, int RT>
+struct __align__(16) Ctrl {
+  uint64_t full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
+  unsigned long long vmask[Cfg<D>::kStages];    // rows of the stage that are keys of its item
+  int abort_flag;
+  int32_t status;
+  int flag[2];                                  // by segment parity: non-finite drafts taken out
+  float m[kWarps][RT], l[kWarps][RT];
+  float o[RT][D + 4];
+};
+
+template <int D, int RT>
+constexpr size_t smem_bytes() { return 1024 + Cfg<D>::kStages * Cfg<D>::kStage + sizeof(Ctrl<D, RT>); }
+
+}  // namespace
+
+template <int D, int RT, bool F16, bool LIST>
+__global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
+    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+    const __grid_constant__ PagedArgs a) {
+  using C = Cfg<D>;
+  constexpr int NT = RT / 8;                    // MMA column tiles of the rows
+  constexpr int DM = D / 16;                    // MMA row tiles of the head dim
+  constexpr float kShift = F16 ? 14.f : 0.f;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctrl<D, RT>& c = *reinterpret_cast<Ctrl<D, RT>*>(sm + C::kStages * C::kStage);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      tc::mbar_init(&c.full[s], 1);
+      tc::mbar_init(&c.empty[s], kWarps / 2);
+    }
+    c.abort_flag = 0;
+    c.status = 0;
+    c.flag[0] = c.flag[1] = 0;
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  volatile int* abort_flag = &c.abort_flag;
+
+  Walk<LIST, RT> w;
+  w.init(a);
+  const long long x0 = w.start(blockIdx.x), x1 = blockIdx.x < w.n_cta ? w.start(blockIdx.x + 1) : x0;
+  int tiles_issued = 0;
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    if (lane == 0) {
+      tc::prefetch_tmap(&tmk);
+      tc::prefetch_tmap(&tmv);
+    }
+    const int page = a.g.page, rpb = page < kTileKeys ? page : kTileKeys, npt = kTileKeys / rpb;
+    int n = 0;                                  // tiles so far
+    bool ok = true;
+    Item it;
+    if (x0 < x1) w.locate(a, x0, it);
+    for (long long x = x0; ok && x < x1;) {
+      const long long xe = min(x1, it.first + it.n_tiles);
+      int cnt;
+      bool bad;
+      const int live = item_live_tiles<LIST>(a, it, cnt, bad);
+      const int ta = (int)(x - it.first), tb = min((int)(xe - it.first), live);
+      const int32_t* table = a.g.table + (size_t)it.b * a.g.max_pages;
+      const int32_t* list = LIST ? a.kv_idx + (((size_t)it.b * a.g.Hkv + it.h) * a.g.T + it.t) * a.W : nullptr;
+      const int limit = LIST ? it.base + it.t + 1 : it.base + it.ql;     // positions below it are keys
+      // lane i: box (i % npt) of tile t0 + i / npt
+      const int per_load = 32 / npt;
+      for (int t0 = ta; ok && t0 < tb; t0 += per_load) {
+        const int tile = t0 + lane / npt;
+        const int slot_row = tile * kTileKeys + (lane % npt) * rpb;      // row in the item's page order
+        const int e = slot_row / page, off = slot_row % page;
+        int rows = 0, y = 0;
+        if (tile < tb) {
+          int j = e;
+          bool in = true;
+          if (LIST) {
+            in = e < cnt;
+            if (in) {
+              j = list[e];
+              if (j < 0 || (long long)j * page >= limit) {
+                bad = true;
+                in = false;
+              }
+            }
+          }
+          if (in) {
+            rows = min(max(limit - (j * page + off), 0), rpb);
+            if (rows > 0) {
+              const int pg = table[j];
+              if (pg < 0 || pg >= a.g.n_pages) {
+                bad = true;
+                rows = 0;
+              }
+              y = (int)(((long long)pg * a.g.Hkv + it.h) * page) + off;
+            }
+          }
+        }
+        unsigned long long bits = rows == 0 ? 0 : (rows == 64 ? ~0ull : (1ull << rows) - 1) << ((lane % npt) * rpb);
+        const int n_here = min(per_load, tb - t0);
+        for (int i = 0; i < n_here; ++i) {
+          const int s = n % C::kStages;
+          if (n >= C::kStages) {
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&c.empty[s], ((n / C::kStages) - 1) & 1, abort_flag, &c.status));
+            if (!ok) break;
+          }
+          const bool mine = lane / npt == i;
+          const unsigned boxes = __ballot_sync(0xffffffffu, mine && rows > 0);
+          const unsigned lo = __reduce_or_sync(0xffffffffu, mine ? (unsigned)bits : 0u);
+          const unsigned hi = __reduce_or_sync(0xffffffffu, mine ? (unsigned)(bits >> 32) : 0u);
+          if (lane == 0) {
+            c.vmask[s] = ((unsigned long long)hi << 32) | lo;
+            tc::mbar_arrive_expect_tx(&c.full[s], (uint32_t)(__popc(boxes) * rpb) * 2u * D * 2u);
+          }
+          __syncwarp();
+          if (mine && rows > 0) {
+            uint8_t* kd = sm + s * C::kStage + (lane % npt) * rpb * 128;
+#pragma unroll
+            for (int hh = 0; hh < C::kHalves; ++hh) {
+              tc::tma_load_2d(kd + hh * C::kHalf, &tmk, hh * 64, y, &c.full[s]);
+              tc::tma_load_2d(kd + C::kTile + hh * C::kHalf, &tmv, hh * 64, y, &c.full[s]);
+            }
+          }
+          ++n;
+        }
+      }
+      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&c.status, BSA_DEV_BAD_INDEX);
+      x = xe;
+      if (x < x1) w.next(a, it);
+    }
+    tiles_issued = n;
+  } else {
+    // ---------------- compute ----------------
+    const int cw = warp - 1, group = cw / 4, kw = cw % 4;
+    const int g8 = lane >> 2, tig = lane & 3;
+    const uint32_t sStages = tc::smem_u32(sm);
+    const uint32_t rowK = (uint32_t)(16 * kw + (lane & 7) + ((lane >> 3) & 1) * 8) * 128u;
+    const uint32_t rowV = (uint32_t)(16 * kw + (lane & 7) + (lane >> 4) * 8) * 128u;
+    const uint32_t selK = (uint32_t)(lane >> 4), selV = (uint32_t)((lane >> 3) & 1);
+    const uint32_t sw = (uint32_t)(lane & 7);
+    const float sl2 = a.scale_log2;
+    int n = 0, seg = 0;
+    bool ok = true;
+    Item it;
+    if (x0 < x1) w.locate(a, x0, it);
+    for (long long x = x0; x < x1; ++seg) {
+      const long long xe = min(x1, it.first + it.n_tiles);
+      int cnt;
+      bool bad;
+      const int live = item_live_tiles<LIST>(a, it, cnt, bad);
+      const int ta = (int)(x - it.first), tend = (int)(xe - it.first), tb = min(tend, live);
+      if (!LIST || it.t < it.ql) {
+        // Q as the B operand: column = row of the item, k = head dim
+        uint32_t qf[D / 16][NT][2];
+        int tq[NT][2];                           // tokens of this thread's columns 8 nt + 2 tig (+1)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = 8 * nt + g8;
+          int head, t;
+          row_of<LIST>(a, it, r < it.rows ? r : 0, head, t);
+          const uint32_t* qr = reinterpret_cast<const uint32_t*>(
+              a.q + (((size_t)it.b * a.Hq + head) * a.g.T + t) * D);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) qf[kk][nt][j] = r < it.rows ? qr[8 * kk + 4 * j + tig] : 0u;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int rc = 8 * nt + 2 * tig + j;
+            int hd;
+            row_of<LIST>(a, it, rc < it.rows ? rc : 0, hd, tq[nt][j]);
+          }
+        }
+        float o[DM][NT][4];
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          m[nt][0] = m[nt][1] = -INFINITY;
+          l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+          for (int dm = 0; dm < DM; ++dm)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[dm][nt][i] = 0.f;
+        }
+
+        for (int tile = ta; tile < tb; ++tile, ++n) {
+          if ((n & 1) != group) continue;
+          const int s = n % C::kStages;
+          if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&c.full[s], (n / C::kStages) & 1, abort_flag, &c.status));
+          if (!ok) continue;                     // still joins the barriers below
+          const uint32_t kb = sStages + s * C::kStage, vb = kb + C::kTile;
+          const unsigned vm = (unsigned)(c.vmask[s] >> (16 * kw)) & 0xffffu;      // this warp's keys
+          const int pos0 = tile * kTileKeys + 16 * kw;                            // whole cache only
+          const bool drafts = !LIST && pos0 + 16 > it.base;
+          if (vm != 0xffffu || (drafts && (a.mask || it.ql > 1))) {
+            // rows that are no keys get V = 0; non-finite values of drafted rows are taken out
+            bool found = false;
+            for (int r = 0; r < 16; ++r) {
+              const bool key = (vm >> r) & 1;
+              if (key && !(drafts && pos0 + r >= it.base)) continue;
+              for (int ch = lane; ch < D / 8; ch += 32) {
+                uint4* p = reinterpret_cast<uint4*>(sm + (vb - sStages) + (ch >> 3) * C::kHalf + (16 * kw + r) * 128 +
+                                                    (((ch & 7) ^ (r & 7)) << 4));
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (key) {
+                  v = *p;
+                  found |= clear_nonfinite<F16>(v.x) | clear_nonfinite<F16>(v.y) |
+                           clear_nonfinite<F16>(v.z) | clear_nonfinite<F16>(v.w);
+                }
+                *p = v;
+              }
+            }
+            if (found) atomicOr(&c.flag[seg & 1], 1);
+            tc::fence_proxy_async_smem();        // the stage is written by TMA next
+            __syncwarp();
+          }
+          // S = K Q^T, two accumulator chains per column tile
+          float sc[2][NT][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sc[j][nt][i] = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t af[4];
+            const uint32_t chunk = (uint32_t)(2 * (kk & 3)) + selK;
+            ldsm4(kb + (uint32_t)(kk >> 2) * C::kHalf + rowK + ((chunk ^ sw) << 4), af);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<F16>(sc[kk & 1][nt], af, qf[kk][nt][0], qf[kk][nt][1]);
+          }
+          // sv[nt][i]: key g8 (i < 2) or g8 + 8, columns 8 nt + 2 tig + (i & 1)
+          float sv[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sv[nt][i] = sc[0][nt][i] + sc[1][nt][i];
+          if (vm != 0xffffu || drafts) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int kr = g8 + 8 * (i >> 1);
+              const bool key = (vm >> kr) & 1;
+              const int dj = pos0 + kr - it.base;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                bool see = key;
+                if (!LIST && see && dj >= 0) see = sees_draft(a, it.b, tq[nt][i & 1], dj);
+                if (!see) sv[nt][i] = -INFINITY;
+              }
+            }
+          }
+          // the maximum is exact, and reduced over the warp only when some score passes it
+          float al[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float b0 = fmaxf(sv[nt][0], sv[nt][2]), b1 = fmaxf(sv[nt][1], sv[nt][3]);
+            al[nt][0] = al[nt][1] = 1.f;
+            if (__any_sync(0xffffffffu, b0 * sl2 > m[nt][0] || b1 * sl2 > m[nt][1])) {
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) {
+                b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, off));
+                b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, off));
+              }
+              const float t0 = b0 * sl2, t1 = b1 * sl2;
+              if (t0 > m[nt][0]) { al[nt][0] = m[nt][0] == -INFINITY ? 0.f : ex2(m[nt][0] - t0); m[nt][0] = t0; }
+              if (t1 > m[nt][1]) { al[nt][1] = m[nt][1] == -INFINITY ? 0.f : ex2(m[nt][1] - t1); m[nt][1] = t1; }
+              if (al[nt][0] != 1.f || al[nt][1] != 1.f) {
+#pragma unroll
+                for (int dm = 0; dm < DM; ++dm) {
+                  o[dm][nt][0] *= al[nt][0]; o[dm][nt][1] *= al[nt][1];
+                  o[dm][nt][2] *= al[nt][0]; o[dm][nt][3] *= al[nt][1];
+                }
+              }
+            }
+          }
+          // P = hi + lo in 16 bits each, as the B operand of O^T += V^T P^T
+          uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float z0 = kShift - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]);
+            const float z1 = kShift - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(sv[nt][i], sl2, (i & 1) ? z1 : z0));
+            l[nt][0] = fmaf(l[nt][0], al[nt][0], p[0] + p[2]);
+            l[nt][1] = fmaf(l[nt][1], al[nt][1], p[1] + p[3]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t h = pack_16<F16>(p[2 * u], p[2 * u + 1]);
+              const uint32_t r = pack_16<F16>(p[2 * u] - cvt_f32<F16>((uint16_t)h),
+                                              p[2 * u + 1] - cvt_f32<F16>((uint16_t)(h >> 16)));
+              ph[nt][u] = movm_t(h);
+              pl[nt][u] = movm_t(r);
+            }
+          }
+#pragma unroll
+          for (int dm = 0; dm < DM; ++dm) {
+            uint32_t af[4];
+            const uint32_t chunk = (uint32_t)(2 * (dm & 3)) + selV;
+            ldsm4_t(vb + (uint32_t)(dm >> 2) * C::kHalf + rowV + ((chunk ^ sw) << 4), af);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816<F16>(o[dm][nt], af, ph[nt][0], ph[nt][1]);
+              mma16816<F16>(o[dm][nt], af, pl[nt][0], pl[nt][1]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&c.empty[s]);
+        }
+
+        // ---- join the eight states ----
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
+            if (g8 == 0) {
+              c.m[cw][8 * nt + 2 * tig + j] = m[nt][j];
+              c.l[cw][8 * nt + 2 * tig + j] = l[nt][j];
+            }
+          }
+        }
+        compute_sync();
+        float f[NT][2];                          // 2^(m - maximum over the warps)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kWarps; ++u) mx = fmaxf(mx, c.m[u][8 * nt + 2 * tig + j]);
+            f[nt][j] = m[nt][j] == -INFINITY ? 0.f : ex2(m[nt][j] - mx);
+          }
+        // eight turns: in each, every warp adds another eighth of its O (in a fixed order per eighth)
+#pragma unroll 1
+        for (int turn = 0; turn < kWarps; ++turn) {
+          const int e8 = (cw + turn) % kWarps;
+#pragma unroll
+          for (int dm = 0; dm < DM; ++dm)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              if ((DM == 8 ? dm : 2 * dm + hf) != e8) continue;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  float* p = &c.o[8 * nt + 2 * tig + j][16 * dm + 8 * hf + g8];
+                  const float v = o[dm][nt][2 * hf + j] * f[nt][j];
+                  *p = turn == 0 ? v : *p + v;
+                }
+            }
+          compute_sync();
+        }
+        // ---- result, or partial result ----
+        const int tid = threadIdx.x - 32;
+        const bool whole = ta == 0 && tend == it.n_tiles;
+        const int fixup = *(volatile int*)&c.flag[seg & 1];
+        const int slot = 2 * blockIdx.x + (ta == 0 ? 1 : 0);
+        for (int i = tid; i < RT * (D / 4); i += 32 * kWarps) {
+          const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
+          if (r >= it.rows) break;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < kWarps; ++u) mx = fmaxf(mx, c.m[u][r]);
+          float ls = 0.f;
+#pragma unroll
+          for (int u = 0; u < kWarps; ++u) ls += c.m[u][r] == -INFINITY ? 0.f : c.l[u][r] * ex2(c.m[u][r] - mx);
+          float4 v = *reinterpret_cast<const float4*>(&c.o[r][d4]);
+          if (whole) {
+            int head, t;
+            row_of<LIST>(a, it, r, head, t);
+            const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
+            const float inv = ls == 0.f ? 0.f : 1.f / ls;
+            float x4[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+            if (!LIST && fixup) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) x4[u] += nonfinite_drafts<F16>(a, it, t, d4 + u);
+            }
+            uint2 pk = make_uint2(pack_16<F16>(x4[0], x4[1]), pack_16<F16>(x4[2], x4[3]));
+            if (ok) *reinterpret_cast<uint2*>(a.out + row * D + d4) = pk;
+            if (ok && d4 == 0 && a.lse)
+              a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
+          } else {
+            *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * RT + r) * D + d4) = v;
+            if (d4 == 0) {
+              a.part_ml[((size_t)slot * RT + r) * 2] = mx;
+              a.part_ml[((size_t)slot * RT + r) * 2 + 1] = ls;
+            }
+          }
+        }
+        if (!whole && tid == 0) a.part_flag[slot] = fixup;
+        compute_sync();
+        if (tid == 0) c.flag[seg & 1] = 0;       // next used two segments on, behind barriers
+      }
+      x = xe;
+      if (x < x1) w.next(a, it);
+    }
+  }
+
+  // ---------------- teardown ----------------
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int t = max(0, tiles_issued - C::kStages); t < tiles_issued; ++t)
+      tc::mbar_wait_timed(&c.full[t % C::kStages], (t / C::kStages) & 1);
+    a.cta_status[blockIdx.x] = c.status;
+  }
+}
+
+// ---------------------------------------------------------------------------
+
+template <int RT, bool F16, bool LIST>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedArgs a) {
+  constexpr float kShift = F16 ? 14.f : 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (c == 0 && blockIdx.y == 0 && warp == 0) {
+    int st = 0;
+    for (int i = lane; i < a.n_cta; i += 32) st |= a.cta_status[i];
+    for (int b = lane; b < a.g.slots; b += 32) {
+      int base, ql;
+      if (!query_span(a.g, b, base, ql)) st |= BSA_DEV_BAD_INDEX;
+    }
+    st = __reduce_or_sync(0xffffffffu, st);
+    if (lane == 0) *a.dev_status = st;
+  }
+  Walk<LIST, RT> w;
+  w.init(a);
+  if (c >= w.n_cta) return;
+  const long long x0 = w.start(c), x1 = w.start(c + 1);
+  if (x0 >= x1) return;
+  Item it;
+  w.locate(a, x0, it);
+  const long long xs = it.first, xe = it.first + it.n_tiles;
+  if (xs == x0 || xe > x1) return;               // starts here, or ends later
+  if (LIST && it.t >= it.ql) return;
+  const int r = blockIdx.y * 4 + warp;
+  if (r >= it.rows) return;
+  int c0 = (int)(xs * w.n_cta / w.total);
+  while (c0 > 0 && w.start(c0) > xs) --c0;
+  while (w.start(c0 + 1) <= xs) ++c0;
+  // maximum and flags over the parts (c0: slot 1, the others: slot 0; none of them is empty
+  // between the item's first tile and this CTA's)
+  float mx = -INFINITY;
+  int flag = 0;
+  for (int i = c0 + lane; i <= c; i += 32) {
+    const int slot = 2 * i + (i == c0 ? 1 : 0);
+    mx = fmaxf(mx, a.part_ml[((size_t)slot * RT + r) * 2]);
+    flag |= a.part_flag[slot];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  flag = __reduce_or_sync(0xffffffffu, flag);
+  const int d = a.g.d;
+  float ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = c0; i <= c; ++i) {
+    const int slot = 2 * i + (i == c0 ? 1 : 0);
+    const size_t row = (size_t)slot * RT + r;
+    const float m = a.part_ml[row * 2], l = a.part_ml[row * 2 + 1];
+    const float f = m == -INFINITY ? 0.f : exp2f(m - mx);
+    ls += l * f;
+    const float* po = a.part_o + row * d;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (lane + 32 * u < d) acc[u] += po[lane + 32 * u] * f;
+  }
+  int head, t;
+  row_of<LIST>(a, it, r, head, t);
+  const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
+  const float inv = ls == 0.f ? 0.f : 1.f / ls;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (lane + 32 * u >= d) continue;
+    float x = acc[u] * inv;
+    if (!LIST && flag) x += nonfinite_drafts<F16>(a, it, t, lane + 32 * u);
+    a.out[row * d + lane + 32 * u] = cvt_16<F16>(x);
+  }
+  if (lane == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 148;
+  return n;
+}
+
+template <int RT, bool F16, bool LIST>
+static cudaError_t join_t(const PagedArgs& a, cudaStream_t st) {
+  // launched behind the attention kernel without waiting for its end; the kernel itself waits
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.n_cta, RT / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<RT, F16, LIST>, a);
+}
+
+template <int RT>
+static cudaError_t join_rt(const PagedArgs& a, bool list, bool f16, cudaStream_t st) {
+  if (f16) return list ? join_t<RT, true, true>(a, st) : join_t<RT, true, false>(a, st);
+  return list ? join_t<RT, false, true>(a, st) : join_t<RT, false, false>(a, st);
+}
+
+cudaError_t launch_paged_join(const PagedArgs& a, int rt, bool list, bool f16, cudaStream_t st) {
+  return rt == 8 ? join_rt<8>(a, list, f16, st) : join_rt<16>(a, list, f16, st);
+}
+
+template <int D, int RT, bool F16, bool LIST>
+static cudaError_t attend_t(const bsa_cache_shape& s, const PagedArgs& a, const void* k, const void* v,
+                            cudaStream_t st) {
+  CUtensorMap mk, mv;
+  const uint64_t rows = (uint64_t)s.n_pages * s.Hkv * s.page;
+  const uint32_t box = s.page < kTileKeys ? s.page : kTileKeys;
+  if (!make_tmap_bf16_2d(&mk, k, rows, D, 64, box) || !make_tmap_bf16_2d(&mv, v, rows, D, 64, box))
+    return cudaErrorInvalidValue;
+  auto kern = paged_attend_kernel<D, RT, F16, LIST>;
+  constexpr size_t smem = smem_bytes<D, RT>();
+  static_assert(smem <= 227 * 1024, "paged attend shared memory");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<a.n_cta, kThreads, smem, st>>>(mk, mv, a);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_paged_join(a, RT, LIST, F16, st);
+}
+
+template <int D, int RT>
+static cudaError_t attend_d(const bsa_cache_shape& s, const PagedArgs& a, const void* k, const void* v,
+                            cudaStream_t st) {
+  const bool f16 = s.dtype == BSA_F16;
+  if (a.kv_idx)
+    return f16 ? attend_t<D, RT, true, true>(s, a, k, v, st) : attend_t<D, RT, false, true>(s, a, k, v, st);
+  return f16 ? attend_t<D, RT, true, false>(s, a, k, v, st) : attend_t<D, RT, false, false>(s, a, k, v, st);
+}
+
+cudaError_t launch_paged_attend_mma(const bsa_cache_shape& s, PagedArgs a, const void* k, const void* v,
+                                    cudaStream_t st) {
+  const int rows = a.kv_idx ? a.G : a.G * a.g.T;
+  if (s.d == 128)
+    return rows <= 8 ? attend_d<128, 8>(s, a, k, v, st) : attend_d<128, 16>(s, a, k, v, st);
+  return rows <= 8 ? attend_d<64, 8>(s, a, k, v, st) : attend_d<64, 16>(s, a, k, v, st);
+}
+
+}  // namespace bsa

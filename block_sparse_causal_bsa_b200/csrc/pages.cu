@@ -1,0 +1,592 @@
+// Pages of a KV cache: forking sequences, growing / shrinking them, copying pages, appending
+// rows and compacting the accepted rows of a draft; ancestor masks of a tree of drafts.
+//
+// The pool and its bookkeeping (page table, lengths, reference counts) live in device memory,
+// so that a whole serving step (resize, append, attend, compact) can sit in one CUDA graph. A
+// page is free when its reference count is 0, and free pages are taken lowest first: the state
+// after a call depends on the state before it alone, not on the order in which threads ran.
+//
+//   fork     table row and length of the parent copied, one reference more per page
+//   resize   shrinking slots give up pages; growing slots then take free ones, and a partly
+//            filled last page that other sequences hold too is replaced by a fresh page (the
+//            (old, new) pair is returned for the copy of its contents, layer by layer)
+//   copy     K, V and bounds of page old -> new
+//   append   rows of new tokens into their pages, and the pages' channel bounds extended
+//   compact  rows base + keep[i] -> base + i, and the touched pages' bounds recomputed
+//
+// All of them move bytes and compute nothing but minima and maxima: the copies are bound by
+// memory bandwidth, the bookkeeping by latency (one CTA, a handful of barriers).
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace bsa {
+
+namespace {
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// ---------------------------------------------------------------------------
+// packed minimum / maximum of two 16-bit floats, NaN if either is NaN
+
+template <bool F16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (F16) asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (F16) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Channel bounds of eight channels per thread, over the rows a thread has seen.
+template <bool F16>
+struct Bounds8 {
+  uint32_t lo[4], hi[4];
+  __device__ void reset() {
+    const uint32_t pinf = F16 ? 0x7c007c00u : 0x7f807f80u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { lo[i] = pinf; hi[i] = pinf | 0x80008000u; }
+  }
+  __device__ void add(const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { lo[i] = min2<F16>(lo[i], w[i]); hi[i] = max2<F16>(hi[i], w[i]); }
+  }
+  __device__ void merge(const uint4& l, const uint4& h) {
+    const uint32_t a[4] = {l.x, l.y, l.z, l.w}, b[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { lo[i] = min2<F16>(lo[i], a[i]); hi[i] = max2<F16>(hi[i], b[i]); }
+  }
+  __device__ uint4 vlo() const { return make_uint4(lo[0], lo[1], lo[2], lo[3]); }
+  __device__ uint4 vhi() const { return make_uint4(hi[0], hi[1], hi[2], hi[3]); }
+};
+
+// Bounds of a block of threads: vectors of a row on consecutive threads (vpr of them), groups
+// of vpr threads on different rows. sh holds 2 uint4 per thread. On return, threads < vpr hold
+// the bounds over every group. All threads call it.
+template <bool F16>
+__device__ void reduce_bounds(Bounds8<F16>& b, uint4* sh, int vpr, int groups) {
+  sh[2 * threadIdx.x] = b.vlo();
+  sh[2 * threadIdx.x + 1] = b.vhi();
+  __syncthreads();
+  if ((int)threadIdx.x < vpr) {
+    for (int g = 1; g < groups; ++g) b.merge(sh[2 * (threadIdx.x + g * vpr)], sh[2 * (threadIdx.x + g * vpr) + 1]);
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// fork: one CTA per slot
+
+__global__ void __launch_bounds__(256) pages_fork_kernel(int slots, int max_pages, int n_pages, int page,
+                                                         int32_t* __restrict__ table, int32_t* seq_len,
+                                                         int32_t* refs, const int32_t* __restrict__ parent,
+                                                         int32_t* dev_status) {
+  const int c = blockIdx.x;
+  const int p = parent[c];
+  if (p < 0) return;
+  // a parent is not a child of the same call (its row and length are then not written here),
+  // and a child starts empty
+  bool ok = p < slots && p != c;
+  ok = ok && parent[p] < 0 && seq_len[c] == 0;
+  const int len = ok ? seq_len[p] : 0;
+  ok = ok && len >= 0 && (long long)len <= (long long)max_pages * page;
+  __syncthreads();                       // every thread has read seq_len[c]
+  if (!ok) {
+    if (threadIdx.x == 0) set_status(dev_status, BSA_DEV_BAD_INDEX);
+    return;
+  }
+  const int n = ceil_div(len, page);
+  for (int j = threadIdx.x; j < max_pages; j += blockDim.x) {
+    int e = -1;
+    if (j < n) {
+      e = table[(size_t)p * max_pages + j];
+      if (e >= 0 && e < n_pages) {
+        atomicAdd(refs + e, 1);
+      } else {
+        e = -1;
+        set_status(dev_status, BSA_DEV_BAD_INDEX);
+      }
+    }
+    table[(size_t)c * max_pages + j] = e;
+  }
+  if (threadIdx.x == 0) seq_len[c] = len;
+}
+
+// ---------------------------------------------------------------------------
+// resize: one CTA
+
+constexpr int kResizeThreads = 1024;
+
+struct ResizeSmem {
+  int warp_sum[32];
+  int status;
+  int taken;                             // pages given out
+  int first[kMaxSlots + 1];              // exclusive prefix of the pages needed
+  int tail[kMaxSlots];                   // shared last page of a growing slot, or -1
+  uint8_t flags[kMaxSlots];              // 1 grows, 2 copy on write, 4 keeps a shared page, 8 granted
+};
+
+// Exclusive prefix of one value per thread; *total gets the sum. All threads call it.
+__device__ int block_exclusive(int v, int* warp_sum, int* total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sum[lane] = s;
+  }
+  __syncthreads();
+  const int r = x - v + (warp ? warp_sum[warp - 1] : 0);
+  *total = warp_sum[31];
+  __syncthreads();
+  return r;
+}
+
+__global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(
+    int slots, int max_pages, int n_pages, int page, int32_t* table, int32_t* seq_len, int32_t* refs,
+    const int32_t* __restrict__ new_len, int32_t* __restrict__ pairs, int32_t* n_free, int32_t* dev_status) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  ResizeSmem& s = *reinterpret_cast<ResizeSmem*>(raw);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const long long max_len = (long long)max_pages * page;
+  if (tid == 0) s.status = s.taken = 0;
+  __syncthreads();
+
+  // 1. shrinking slots give up pages (a warp per slot)
+  for (int t = warp; t < slots; t += kResizeThreads / 32) {
+    const int L = seq_len[t], n = new_len[t];
+    const bool ok = L >= 0 && L <= max_len && n <= max_len;
+    if (!ok && lane == 0) atomicOr(&s.status, BSA_DEV_BAD_INDEX);
+    if (lane == 0) s.flags[t] = ok && n > L ? 1 : 0;
+    if (ok && n >= 0 && n < L) {
+      for (int j = ceil_div(n, page) + lane; j < ceil_div(L, page); j += 32) {
+        int32_t* e = table + (size_t)t * max_pages + j;
+        const int pg = *e;
+        *e = -1;
+        if (pg < 0 || pg >= n_pages) {
+          atomicOr(&s.status, BSA_DEV_BAD_INDEX);
+        } else if (atomicSub(refs + pg, 1) <= 0) {
+          atomicAdd(refs + pg, 1);       // was not held: leave the count as it was
+          atomicOr(&s.status, BSA_DEV_BAD_INDEX);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) seq_len[t] = n;
+    }
+  }
+  __threadfence();
+  __syncthreads();
+
+  // 2. growing slots whose partly filled last page has other holders
+  for (int t = tid; t < slots; t += kResizeThreads) {
+    int tail = -1;
+    if (s.flags[t] & 1) {
+      const int L = seq_len[t];
+      if (L % page) {
+        const int pg = table[(size_t)t * max_pages + L / page];
+        if (pg < 0 || pg >= n_pages) {
+          atomicOr(&s.status, BSA_DEV_BAD_INDEX);
+          s.flags[t] = 0;                // not grown
+        } else if (__ldcg(refs + pg) > 1) {
+          tail = pg;
+        }
+      }
+    }
+    s.tail[t] = tail;
+  }
+  __syncthreads();
+  // When every holder of such a page grows, the last of them keeps it and the others copy;
+  // else all of them copy. (The pages go to a prefix of the slots, so if the keeper is
+  // granted its own, every other holder has left.)
+  for (int t = tid; t < slots; t += kResizeThreads) {
+    const int pg = s.tail[t];
+    if (pg < 0) continue;
+    int holders = 0;
+    bool later = false;
+    for (int u = 0; u < slots; ++u) {
+      if (s.tail[u] == pg) {
+        ++holders;
+        later |= u > t;
+      }
+    }
+    s.flags[t] |= (holders == __ldcg(refs + pg) && !later) ? 4 : 2;
+  }
+  __syncthreads();
+
+  // 3. pages needed per slot, in slot order
+  const int per = ceil_div(slots, kResizeThreads);
+  const int t0 = min(tid * per, slots), t1 = min(t0 + per, slots);
+  int mine = 0;
+  for (int t = t0; t < t1; ++t) {
+    int need = 0;
+    if (s.flags[t] & 1) {
+      need = ceil_div(new_len[t], page) - ceil_div(seq_len[t], page) + ((s.flags[t] >> 1) & 1);
+    }
+    s.first[t] = need;
+    mine += need;
+  }
+  int total;
+  int at = block_exclusive(mine, s.warp_sum, &total);
+  for (int t = t0; t < t1; ++t) {
+    const int need = s.first[t];
+    s.first[t] = at;
+    at += need;
+  }
+  if (tid == 0) s.first[slots] = total;
+
+  // 4. free pages: a contiguous range of the pool per thread (rounded to a multiple of four,
+  // so that it is read 16 bytes at a time), counted, then given out lowest first
+  const int seg = ceil_div(ceil_div(n_pages, kResizeThreads), 4) * 4;
+  const int p0 = min((long long)tid * seg, (long long)n_pages), p1 = min(p0 + seg, n_pages);
+  int free_here = 0;
+  for (int p = p0; p < p1; p += 4) {
+    if (p + 4 <= p1) {
+      const int4 r = __ldcg(reinterpret_cast<const int4*>(refs + p));
+      free_here += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+    } else {
+      for (int i = p; i < p1; ++i) free_here += __ldcg(refs + i) == 0;
+    }
+  }
+  int avail;
+  int rank = block_exclusive(free_here, s.warp_sum, &avail);
+  for (int t = tid; t < slots; t += kResizeThreads) {
+    if (!(s.flags[t] & 1)) continue;
+    const int need = s.first[t + 1] - s.first[t];
+    if ((need == 0 && !(s.flags[t] & 4)) || s.first[t + 1] <= avail) {
+      s.flags[t] |= 8;
+      if (need) atomicAdd(&s.taken, need);
+    } else {
+      atomicOr(&s.status, BSA_DEV_NO_PAGES);
+    }
+  }
+  __syncthreads();
+  for (int p = p0; p < p1 && rank < total; ++p) {
+    if (__ldcg(refs + p) != 0) continue;
+    const int r = rank++;
+    // the slot whose pages include rank r: the last one with first <= r and need > 0
+    int lo = 0, hi = slots;              // first[lo] <= r < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (s.first[mid] <= r) lo = mid;
+      else hi = mid;
+    }
+    if (!(s.flags[lo] & 8)) continue;
+    const int i = r - s.first[lo], cow = (s.flags[lo] >> 1) & 1;
+    const int L = seq_len[lo];
+    refs[p] = 1;
+    if (cow && i == 0) {
+      int32_t* e = table + (size_t)lo * max_pages + L / page;
+      pairs[2 * lo] = *e;
+      pairs[2 * lo + 1] = p;
+      atomicSub(refs + *e, 1);           // stays above 0: another holder keeps the page
+      *e = p;
+    } else {
+      table[(size_t)lo * max_pages + ceil_div(L, page) + i - cow] = p;
+    }
+  }
+  __syncthreads();                       // seq_len is read above
+  for (int t = tid; t < slots; t += kResizeThreads) {
+    if (s.flags[t] & 8) seq_len[t] = new_len[t];
+    if ((s.flags[t] & 10) != 10) pairs[2 * t] = pairs[2 * t + 1] = -1;
+  }
+  if (tid == 0) {
+    if (n_free) *n_free = avail - s.taken;
+    if (dev_status) *dev_status = s.status;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// copy: one CTA per (pair, head)
+
+__global__ void __launch_bounds__(256) pages_copy_kernel(uint4* __restrict__ k, uint4* __restrict__ v,
+                                                         uint4* __restrict__ bounds,
+                                                         const int2* __restrict__ pairs, int n_pairs,
+                                                         int n_pages, int Hkv, int vec_page, int vec_bounds,
+                                                         int32_t* dev_status) {
+  const int i = blockIdx.x / Hkv, h = blockIdx.x % Hkv;
+  const int2 pr = pairs[i];
+  if (pr.x < 0 && pr.y < 0) return;
+  // the destination must be no page that another pair reads, nor one that an earlier pair
+  // writes: the copies run in any order
+  bool bad = pr.x < 0 || pr.x >= n_pages || pr.y < 0 || pr.y >= n_pages;
+  for (int j = threadIdx.x; j < n_pairs; j += blockDim.x) {
+    const int2 o = pairs[j];
+    bad |= o.x == pr.y || (o.y == pr.y && j < i);
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) set_status(dev_status, BSA_DEV_BAD_INDEX);
+    return;
+  }
+  const size_t src = (size_t)pr.x * Hkv + h, dst = (size_t)pr.y * Hkv + h;
+  const uint4* ks = k + src * vec_page;
+  const uint4* vs = v + src * vec_page;
+  uint4* kd = k + dst * vec_page;
+  uint4* vd = v + dst * vec_page;
+  constexpr int U = 4;
+  for (int e = threadIdx.x; e < vec_page; e += U * blockDim.x) {
+    uint4 a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = e + u * blockDim.x;
+      if (x < vec_page) { a[u] = __ldcs(ks + x); b[u] = __ldcs(vs + x); }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = e + u * blockDim.x;
+      if (x < vec_page) { __stcs(kd + x, a[u]); __stcs(vd + x, b[u]); }
+    }
+  }
+  if (bounds)
+    for (int e = threadIdx.x; e < vec_bounds; e += blockDim.x) bounds[dst * vec_bounds + e] = bounds[src * vec_bounds + e];
+}
+
+// ---------------------------------------------------------------------------
+// Checks of append and compact that one CTA makes for the whole call (the others skip what
+// they may not touch without a word): lengths, and the table entries of the call's tokens.
+__device__ int check_spans(const CacheGeom& g) {
+  int st = 0;
+  for (int b = threadIdx.x; b < g.slots; b += blockDim.x) {
+    int base, ql;
+    if (!query_span(g, b, base, ql)) st |= BSA_DEV_BAD_INDEX;
+    if (ql == 0) continue;
+    for (int j = base / g.page; j <= (base + ql - 1) / g.page; ++j) {
+      const int pg = g.table[(size_t)b * g.max_pages + j];
+      if (pg < 0 || pg >= g.n_pages) st |= BSA_DEV_BAD_INDEX;
+    }
+  }
+  return st;
+}
+
+// append: one CTA per (slot, head, touched page), and one that checks
+
+constexpr int kAppendThreads = 128;
+
+template <bool F16>
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(
+    CacheGeom g, int touch, const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+    uint4* __restrict__ k, uint4* __restrict__ v, uint4* __restrict__ bounds, int32_t* dev_status) {
+  __shared__ uint4 sh[2 * kAppendThreads];
+  if (blockIdx.x == gridDim.x - 1) {
+    const int st = __syncthreads_or(check_spans(g));
+    if (threadIdx.x == 0) *dev_status = st ? BSA_DEV_BAD_INDEX : 0;
+    return;
+  }
+  int x = blockIdx.x;
+  const int ti = x % touch;
+  x /= touch;
+  const int h = x % g.Hkv, b = x / g.Hkv;
+  int base, ql;
+  if (!query_span(g, b, base, ql) || ql == 0) return;
+  const int j = base / g.page + ti;
+  const int lo = max(base, j * g.page), hi = min(base + ql, (j + 1) * g.page);   // positions
+  if (lo >= hi) return;
+  const int pg = g.table[(size_t)b * g.max_pages + j];
+  if (pg < 0 || pg >= g.n_pages) return;
+  const int vpr = g.d / 8, groups = kAppendThreads / vpr;
+  const int vec = threadIdx.x % vpr, row = threadIdx.x / vpr;
+  const size_t src = (((size_t)b * g.Hkv + h) * g.T + (lo - base)) * vpr + vec;
+  const size_t dst = (((size_t)pg * g.Hkv + h) * g.page + (lo - j * g.page)) * vpr + vec;
+  Bounds8<F16> bd;
+  bd.reset();
+#pragma unroll 4
+  for (int r = row; r < hi - lo; r += groups) {
+    const uint4 a = __ldcs(k_new + src + (size_t)r * vpr), c = __ldcs(v_new + src + (size_t)r * vpr);
+    k[dst + (size_t)r * vpr] = a;
+    v[dst + (size_t)r * vpr] = c;
+    bd.add(a);
+  }
+  if (!bounds) return;
+  reduce_bounds<F16>(bd, sh, vpr, groups);
+  if ((int)threadIdx.x < vpr) {
+    uint4* bp = bounds + ((size_t)pg * g.Hkv + h) * 2 * vpr + threadIdx.x;
+    if (lo > j * g.page) bd.merge(bp[0], bp[vpr]);     // rows before the call stay covered
+    bp[0] = bd.vlo();
+    bp[vpr] = bd.vhi();
+  }
+}
+
+// compact: one CTA per (slot, head), and one that checks
+
+constexpr int kCompactThreads = 256;
+
+// Whether this thread's share (i0, i0 + step, ...) of a keep list breaks the rule: ascending,
+// and within the call's tokens.
+__device__ __forceinline__ bool keep_bad(const int32_t* keep, int nk, int ql, int i0, int step) {
+  bool bad = nk < 0 || nk > ql;
+  if (!bad)
+    for (int i = i0; i < nk; i += step) bad |= keep[i] < 0 || keep[i] >= ql || (i > 0 && keep[i] <= keep[i - 1]);
+  return bad;
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(
+    CacheGeom g, const int32_t* __restrict__ keep, const int32_t* __restrict__ n_keep, uint4* k, uint4* v,
+    uint4* __restrict__ bounds, int32_t* dev_status) {
+  __shared__ uint4 sh[2 * kCompactThreads];
+  if (blockIdx.x == gridDim.x - 1) {
+    int st = check_spans(g);
+    for (int b = threadIdx.x / 32; b < g.slots; b += kCompactThreads / 32) {
+      int base, ql;
+      query_span(g, b, base, ql);
+      if (ql > 0 && keep_bad(keep + (size_t)b * g.T, n_keep[b], ql, threadIdx.x % 32, 32)) st |= BSA_DEV_BAD_INDEX;
+    }
+    st = __syncthreads_or(st);
+    if (threadIdx.x == 0) *dev_status = st ? BSA_DEV_BAD_INDEX : 0;
+    return;
+  }
+  const int b = blockIdx.x / g.Hkv, h = blockIdx.x % g.Hkv;
+  int base, ql;
+  if (!query_span(g, b, base, ql) || ql == 0) return;
+  const int32_t* kp = keep + (size_t)b * g.T;
+  const int32_t* tb = g.table + (size_t)b * g.max_pages;
+  const int nk = n_keep[b];
+  bool bad = false;
+  for (int j = base / g.page + threadIdx.x; j <= (base + ql - 1) / g.page; j += blockDim.x)
+    bad |= tb[j] < 0 || tb[j] >= g.n_pages;
+  bad |= keep_bad(kp, nk, ql, threadIdx.x, blockDim.x);
+  if (__syncthreads_or(bad)) return;
+
+  const int vpr = g.d / 8, groups = kCompactThreads / vpr;
+  const int vec = threadIdx.x % vpr, row = threadIdx.x / vpr;
+  auto at = [&](int pos) {
+    return (((size_t)tb[pos / g.page] * g.Hkv + h) * g.page + pos % g.page) * vpr + vec;
+  };
+  // Chunks of rows in ascending order, each read whole before it is written: row i goes to
+  // base + i <= base + keep[i], so no chunk overwrites a row that a later one reads.
+  for (int c0 = 0; c0 < nk; c0 += groups) {
+    const int i = c0 + row;
+    const int from = i < nk ? kp[i] : i;
+    uint4 a, c;
+    size_t to = 0;
+    if (from != i) {
+      const size_t src = at(base + from);
+      to = at(base + i);
+      a = k[src];
+      c = v[src];
+    }
+    __syncthreads();
+    if (from != i) {
+      k[to] = a;
+      v[to] = c;
+    }
+    __syncthreads();
+  }
+  if (!bounds) return;
+  const int end = base + nk;
+  for (int j = base / g.page; j * g.page < end; ++j) {
+    Bounds8<F16> bd;
+    bd.reset();
+    for (int p = j * g.page + row; p < min(end, (j + 1) * g.page); p += groups) bd.add(k[at(p)]);
+    reduce_bounds<F16>(bd, sh, vpr, groups);
+    if ((int)threadIdx.x < vpr) {
+      uint4* bp = bounds + ((size_t)tb[j] * g.Hkv + h) * 2 * vpr + threadIdx.x;
+      bp[0] = bd.vlo();
+      bp[vpr] = bd.vhi();
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// tree masks: bit j of row t is set when j is t or an ancestor of t. One CTA per sequence, a
+// thread per mask word, which walks up from its token.
+
+__global__ void __launch_bounds__(256) tree_mask_kernel(int T, int words, const int32_t* __restrict__ parents,
+                                                        const int32_t* __restrict__ q_len,
+                                                        unsigned long long* __restrict__ mask,
+                                                        int32_t* dev_status) {
+  __shared__ int16_t par[kMaxQueryTokens];
+  const int b = blockIdx.x;
+  int ql = q_len ? q_len[b] : T;
+  bool bad = ql < 0 || ql > T;
+  if (bad) ql = 0;
+  for (int t = threadIdx.x; t < ql; t += blockDim.x) {
+    const int p = parents[(size_t)b * T + t];
+    const bool ok = p >= -1 && p < t;                  // parents come first: the walk ends
+    bad |= !ok;
+    par[t] = ok ? (int16_t)p : (int16_t)-1;
+  }
+  if (__syncthreads_or(bad) && threadIdx.x == 0) set_status(dev_status, BSA_DEV_BAD_INDEX);
+  for (int i = threadIdx.x; i < T * words; i += blockDim.x) {
+    const int t = i / words, w = i % words;
+    unsigned long long bits = 0;
+    if (t < ql)
+      for (int x = t; x >= 0; x = par[x])
+        if ((x >> 6) == w) bits |= 1ull << (x & 63);
+    mask[(size_t)b * T * words + i] = bits;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_pages_fork(int slots, int max_pages, int n_pages, int page, int32_t* table,
+                              int32_t* seq_len, int32_t* refs, const int32_t* parent, int32_t* dev_status,
+                              cudaStream_t st) {
+  pages_fork_kernel<<<slots, 256, 0, st>>>(slots, max_pages, n_pages, page, table, seq_len, refs, parent,
+                                           dev_status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_resize(int slots, int max_pages, int n_pages, int page, int32_t* table,
+                                int32_t* seq_len, int32_t* refs, const int32_t* new_len, int32_t* pairs,
+                                int32_t* n_free, int32_t* dev_status, cudaStream_t st) {
+  static_assert(sizeof(ResizeSmem) <= 48 * 1024, "resize shared memory");
+  pages_resize_kernel<<<1, kResizeThreads, sizeof(ResizeSmem), st>>>(
+      slots, max_pages, n_pages, page, table, seq_len, refs, new_len, pairs, n_free, dev_status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_copy(const bsa_cache_shape& s, void* k, void* v, void* bounds, const int32_t* pairs,
+                              int n_pairs, int32_t* dev_status, cudaStream_t st) {
+  const int vpr = s.d / 8;
+  pages_copy_kernel<<<(unsigned)((long long)n_pairs * s.Hkv), 256, 0, st>>>(
+      (uint4*)k, (uint4*)v, (uint4*)bounds, (const int2*)pairs, n_pairs, s.n_pages, s.Hkv, s.page * vpr,
+      2 * vpr, dev_status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append(const bsa_cache_shape& s, const CacheGeom& g, const void* k_new,
+                                const void* v_new, void* k, void* v, void* bounds, int32_t* dev_status,
+                                cudaStream_t st) {
+  const int touch = (g.T + g.page - 2) / g.page + 1;   // pages that T consecutive positions can touch
+  const unsigned grid = (unsigned)((long long)g.slots * g.Hkv * touch + 1);
+  auto kern = s.dtype == BSA_F16 ? cache_append_kernel<true> : cache_append_kernel<false>;
+  kern<<<grid, kAppendThreads, 0, st>>>(g, touch, (const uint4*)k_new, (const uint4*)v_new, (uint4*)k,
+                                        (uint4*)v, (uint4*)bounds, dev_status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_compact(const bsa_cache_shape& s, const CacheGeom& g, const int32_t* keep,
+                                 const int32_t* n_keep, void* k, void* v, void* bounds, int32_t* dev_status,
+                                 cudaStream_t st) {
+  const unsigned grid = (unsigned)((long long)g.slots * g.Hkv + 1);
+  auto kern = s.dtype == BSA_F16 ? cache_compact_kernel<true> : cache_compact_kernel<false>;
+  kern<<<grid, kCompactThreads, 0, st>>>(g, keep, n_keep, (uint4*)k, (uint4*)v, (uint4*)bounds, dev_status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tree_mask(int B, int T, const int32_t* parents, const int32_t* q_len,
+                             unsigned long long* mask, int32_t* dev_status, cudaStream_t st) {
+  tree_mask_kernel<<<B, 256, 0, st>>>(T, (T + 63) / 64, parents, q_len, mask, dev_status);
+  return cudaGetLastError();
+}
+
+}  // namespace bsa

@@ -1,0 +1,345 @@
+"""Serving from a paged cache: pages of many sequences in one pool, several query tokens a step.
+
+A step, for the sequences ("slots") of a :class:`PagedCache`::
+
+    pairs, n_free, st = paged.resize(cache, new_len)      # pages for the step's tokens
+    for layer in ...:
+        paged.copy_pages(cache, pairs, layer=layer)       # only after a fork: shared last pages
+        paged.append(cache, k_new, v_new, q_len=q_len, layer=layer)
+        out, lse, st = paged.attend_tree(q, cache, mask=mask, q_len=q_len, layer=layer)
+        # or: sel = paged.select_pages(q, cache, cfg, q_len=q_len, layer=layer)
+        #     out, lse, st = paged.attend_pages(q, cache, sel["kv_idx"], sel["kv_cnt"], ...)
+    # after the drafts are verified, per layer:
+        paged.compact(cache, keep, n_keep, q_len=q_len, layer=layer)
+    paged.resize(cache, cache.seq_len - q_len + n_keep)   # the rejected drafts' pages
+
+The calls run on the current stream of the cache's device (or on ``stream``) and return at once.
+Arguments that the host can check raise :class:`BsaError`; what only the device sees is in the
+status tensors returned. ``include/bsa.h`` ("paged cache") says what each call does.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import dataclasses
+import math
+from typing import Optional
+
+import torch
+
+from .binding import (BSA_BF16, BSA_ERR_INVALID_ARG, BSA_ERR_UNSUPPORTED, BSA_F16, BsaError, CacheShape,
+                      PageSelectParams, _check, _empty_bytes, lib)
+
+_DTYPES = {torch.bfloat16: BSA_BF16, torch.float16: BSA_F16}
+
+
+def _bad(msg: str, status: int = BSA_ERR_INVALID_ARG):
+    raise BsaError(status, msg)
+
+
+@dataclasses.dataclass
+class PagedCache:
+    """The pools of all layers, and the bookkeeping they share (device tensors, contiguous).
+
+    k, v [layers, n_pages, Hkv, page, d] (bf16 or fp16); bounds [layers, n_pages, Hkv, 2, d] of the
+    same type or None; page_table [slots, max_pages], seq_len [slots], refs [n_pages] int32."""
+    k: torch.Tensor
+    v: torch.Tensor
+    bounds: Optional[torch.Tensor]
+    page_table: torch.Tensor
+    seq_len: torch.Tensor
+    refs: torch.Tensor
+
+    @classmethod
+    def create(cls, *, layers: int, n_pages: int, Hkv: int, page: int, d: int, slots: int, max_pages: int,
+               dtype: torch.dtype = torch.bfloat16, device="cuda", bounds: bool = True) -> "PagedCache":
+        """An empty cache."""
+        i32 = dict(dtype=torch.int32, device=device)
+        shape = (layers, n_pages, Hkv, page, d)
+        return cls(k=torch.zeros(shape, dtype=dtype, device=device),
+                   v=torch.zeros(shape, dtype=dtype, device=device),
+                   bounds=(torch.zeros(layers, n_pages, Hkv, 2, d, dtype=dtype, device=device) if bounds
+                           else None),
+                   page_table=torch.full((slots, max_pages), -1, **i32),
+                   seq_len=torch.zeros(slots, **i32), refs=torch.zeros(n_pages, **i32))
+
+    def __post_init__(self):
+        if self.k.dim() != 5 or self.k.shape != self.v.shape:
+            _bad("k and v must be [layers, n_pages, Hkv, page, d]")
+        L, P, H, page, d = self.k.shape
+        if self.k.dtype not in _DTYPES:
+            _bad("the paged cache takes bf16 and fp16", BSA_ERR_UNSUPPORTED)
+        _tensor("v", self.v, self.k.shape, self.k.dtype, self.device)
+        _tensor("k", self.k, self.k.shape, self.k.dtype, self.device)
+        if self.bounds is not None:
+            _tensor("bounds", self.bounds, (L, P, H, 2, d), self.k.dtype, self.device)
+        if self.page_table.dim() != 2:
+            _bad("page_table must be [slots, max_pages]")
+        _tensor("page_table", self.page_table, self.page_table.shape, torch.int32, self.device)
+        _tensor("seq_len", self.seq_len, (self.slots,), torch.int32, self.device)
+        _tensor("refs", self.refs, (P,), torch.int32, self.device)
+
+    @property
+    def device(self):
+        return self.k.device
+
+    @property
+    def slots(self) -> int:
+        return self.page_table.shape[0]
+
+    @property
+    def max_pages(self) -> int:
+        return self.page_table.shape[1]
+
+    def shape(self) -> CacheShape:
+        _, P, H, page, d = self.k.shape
+        return CacheShape(P, H, page, d, _DTYPES[self.k.dtype])
+
+    def _layer(self, layer: int):
+        if not 0 <= layer < self.k.shape[0]:
+            _bad(f"layer {layer} of {self.k.shape[0]}")
+        return (self.k[layer].data_ptr(), self.v[layer].data_ptr(),
+                self.bounds[layer].data_ptr() if self.bounds is not None else None)
+
+    def _table(self):
+        return self.slots, self.max_pages, self.k.shape[1], self.k.shape[3]
+
+
+@dataclasses.dataclass
+class PageSelectConfig:
+    """Pages per token (k), of which the first n_first and the last n_last are always kept."""
+    k: int
+    n_first: int = 1
+    n_last: int = 1
+
+
+def _tensor(name: str, t, shape, dtype, device):
+    if not isinstance(t, torch.Tensor):
+        _bad(f"{name} must be a tensor")
+    if t.device != device:
+        _bad(f"{name} is on {t.device}, the cache on {device}")
+    if t.dtype != dtype:
+        _bad(f"{name} must be {dtype}, is {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        _bad(f"{name} must be {list(shape)}, is {list(t.shape)}")
+    if not t.is_contiguous():
+        _bad(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Run on the device, outputs and workspaces allocated for the stream that uses them. Yields
+    the stream's handle."""
+    if device.type != "cuda":
+        _bad(f"the cache is on {device}; the kernels need a GPU")
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream)
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _status(device):
+    return torch.empty(1, dtype=torch.int32, device=device)
+
+
+def _qlen(cache, q_len):
+    return None if q_len is None else _tensor("q_len", q_len, (cache.slots,), torch.int32, cache.device)
+
+
+def fork(cache: PagedCache, parent: torch.Tensor, *, stream=None) -> torch.Tensor:
+    """Slots c with parent[c] >= 0 (int32 [slots]) become copies of their parents, sharing their
+    pages. Returns the status."""
+    p = _tensor("parent", parent, (cache.slots,), torch.int32, cache.device)
+    with _on(cache.device, stream) as s:
+        st = _status(cache.device)
+        _check(lib().bsa_pages_fork(*cache._table(), cache.page_table.data_ptr(), cache.seq_len.data_ptr(),
+                                    cache.refs.data_ptr(), p, st.data_ptr(), s))
+    return st
+
+
+def resize(cache: PagedCache, new_len: torch.Tensor, *, stream=None):
+    """Sets the slots' lengths (int32 [slots]; negative: as it is, 0: freed), taking and giving up
+    pages. Returns (pairs [slots, 2] for copy_pages, free pages left, status)."""
+    n = _tensor("new_len", new_len, (cache.slots,), torch.int32, cache.device)
+    with _on(cache.device, stream) as s:
+        st, n_free = _status(cache.device), _status(cache.device)
+        pairs = torch.empty(cache.slots, 2, dtype=torch.int32, device=cache.device)
+        _check(lib().bsa_pages_resize(*cache._table(), cache.page_table.data_ptr(),
+                                      cache.seq_len.data_ptr(), cache.refs.data_ptr(), n, pairs.data_ptr(),
+                                      n_free.data_ptr(), st.data_ptr(), s))
+    return pairs, n_free, st
+
+
+def copy_pages(cache: PagedCache, pairs: torch.Tensor, *, layer: int = 0, stream=None) -> torch.Tensor:
+    """Copies one layer's pages pairs[i, 0] to pairs[i, 1] (int32 [n, 2]; (-1, -1) is skipped).
+    Returns the status."""
+    if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2:
+        _bad("pairs must be [n, 2]")
+    p = _tensor("pairs", pairs, (pairs.shape[0], 2), torch.int32, cache.device)
+    k, v, b = cache._layer(layer)
+    shape = cache.shape()
+    with _on(cache.device, stream) as s:
+        st = _status(cache.device)
+        if pairs.shape[0] == 0:
+            return st.zero_()
+        _check(lib().bsa_pages_copy(ctypes.byref(shape), k, v, b, p, pairs.shape[0], st.data_ptr(), s))
+    return st
+
+
+def append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, *, q_len=None, layer: int = 0,
+           stream=None) -> torch.Tensor:
+    """Writes k_new, v_new [slots, Hkv, T, d] to the last q_len positions of the slots (resize
+    comes first) and extends their pages' bounds. Returns the status."""
+    _, _, H, _, d = cache.k.shape
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
+        _bad("k_new must be [slots, Hkv, T, d]")
+    T = k_new.shape[2]
+    kn = _tensor("k_new", k_new, (cache.slots, H, T, d), cache.k.dtype, cache.device)
+    vn = _tensor("v_new", v_new, (cache.slots, H, T, d), cache.k.dtype, cache.device)
+    ql = _qlen(cache, q_len)
+    k, v, b = cache._layer(layer)
+    shape = cache.shape()
+    with _on(cache.device, stream) as s:
+        st = _status(cache.device)
+        _check(lib().bsa_cache_append(ctypes.byref(shape), cache.slots, cache.max_pages, T, kn, vn, k, v, b,
+                                      cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
+                                      st.data_ptr(), s))
+    return st
+
+
+def compact(cache: PagedCache, keep: torch.Tensor, n_keep: torch.Tensor, *, q_len=None, layer: int = 0,
+            stream=None) -> torch.Tensor:
+    """Moves the rows keep[s, :n_keep[s]] (ascending, int32 [slots, T]) of the last q_len positions
+    of each slot together. Resize to seq_len - q_len + n_keep afterwards. Returns the status."""
+    if not isinstance(keep, torch.Tensor) or keep.dim() != 2:
+        _bad("keep must be [slots, T]")
+    T = keep.shape[1]
+    kp = _tensor("keep", keep, (cache.slots, T), torch.int32, cache.device)
+    nk = _tensor("n_keep", n_keep, (cache.slots,), torch.int32, cache.device)
+    ql = _qlen(cache, q_len)
+    k, v, b = cache._layer(layer)
+    shape = cache.shape()
+    with _on(cache.device, stream) as s:
+        st = _status(cache.device)
+        _check(lib().bsa_cache_compact(ctypes.byref(shape), cache.slots, cache.max_pages, T, kp, nk, k, v, b,
+                                       cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
+                                       st.data_ptr(), s))
+    return st
+
+
+def tree_mask(parents: torch.Tensor, *, q_len=None, stream=None):
+    """Ancestor masks of drafted trees: parents int32 [B, T], -1 for a root. Returns (mask int64
+    [B, T, ceil(T/64)], status)."""
+    if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
+        _bad("parents must be [B, T]")
+    B, T = parents.shape
+    dev = parents.device
+    p = _tensor("parents", parents, (B, T), torch.int32, dev)
+    ql = None if q_len is None else _tensor("q_len", q_len, (B,), torch.int32, dev)
+    with _on(dev, stream) as s:
+        st = _status(dev)
+        mask = torch.empty(B, T, (T + 63) // 64, dtype=torch.int64, device=dev)
+        _check(lib().bsa_tree_mask(B, T, p, ql, mask.data_ptr(), st.data_ptr(), s))
+    return mask, st
+
+
+def _query(q, cache):
+    _, _, H, _, d = cache.k.shape
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        _bad("q must be [slots, Hq, T, d]")
+    Hq, T = q.shape[1], q.shape[2]
+    return Hq, T, _tensor("q", q, (cache.slots, Hq, T, d), cache.k.dtype, cache.device)
+
+
+def _attend(name, q, cache, extra, q_len, layer, scale, out, lse, stream):
+    Hq, T, qp = _query(q, cache)
+    ql = _qlen(cache, q_len)
+    k, v, _ = cache._layer(layer)
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    if out is not None:
+        _tensor("out", out, q.shape, q.dtype, cache.device)
+    if lse is not None:
+        _tensor("lse", lse, q.shape[:3], torch.float32, cache.device)
+    shape = cache.shape()
+    with _on(cache.device, stream) as s:
+        st = _status(cache.device)
+        # rows past q_len are not written: 0 and -inf in tensors made here
+        if out is None:
+            out = torch.empty_like(q) if q_len is None else torch.zeros_like(q)
+        if lse is None:
+            lse = torch.full(q.shape[:3], float("-inf"), dtype=torch.float32, device=q.device) \
+                if q_len is not None else torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        nb = lib().bsa_attend_paged_workspace_bytes(ctypes.byref(shape), cache.slots, cache.max_pages, Hq, T)
+        if nb == 0:
+            _bad(lib().bsa_last_error().decode(), BSA_ERR_UNSUPPORTED)
+        ws = _empty_bytes(nb, cache.device)
+        _check(getattr(lib(), name)(ctypes.byref(shape), cache.slots, cache.max_pages, Hq, T, qp, k, v,
+                                    cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql, *extra, scale,
+                                    out.data_ptr(), lse.data_ptr(), st.data_ptr(), ws.data_ptr(), nb, s))
+    return out, lse, st
+
+
+def attend_tree(q: torch.Tensor, cache: PagedCache, *, mask=None, q_len=None, layer: int = 0,
+                scale: Optional[float] = None, out=None, lse=None, stream=None):
+    """Attention of the last q_len positions (q [slots, Hq, T, d]) over the whole cache of their
+    slots; mask int64 [slots, T, ceil(T/64)] says which drafted tokens see each other (None: a
+    chain). Returns (out, lse, status)."""
+    m = None
+    if mask is not None:
+        _, T, _ = _query(q, cache)
+        m = _tensor("mask", mask, (cache.slots, T, (T + 63) // 64), torch.int64, cache.device)
+    return _attend("bsa_attend_tree", q, cache, (m,), q_len, layer, scale, out, lse, stream)
+
+
+def attend_pages(q: torch.Tensor, cache: PagedCache, kv_idx: torch.Tensor, kv_cnt: torch.Tensor, *,
+                 q_len=None, layer: int = 0, scale: Optional[float] = None, out=None, lse=None, stream=None):
+    """Attention of each token over its listed pages (kv_idx [slots, Hkv, T, W], kv_cnt [slots, Hkv,
+    T], int32). Returns (out, lse, status)."""
+    _, T, _ = _query(q, cache)
+    H = cache.k.shape[2]
+    if not isinstance(kv_idx, torch.Tensor) or kv_idx.dim() != 4:
+        _bad("kv_idx must be [slots, Hkv, T, W]")
+    W = kv_idx.shape[3]
+    i = _tensor("kv_idx", kv_idx, (cache.slots, H, T, W), torch.int32, cache.device)
+    c = _tensor("kv_cnt", kv_cnt, (cache.slots, H, T), torch.int32, cache.device)
+    return _attend("bsa_attend_pages", q, cache, (i, c, W), q_len, layer, scale, out, lse, stream)
+
+
+def select_pages(q: torch.Tensor, cache: PagedCache, cfg: PageSelectConfig, *, q_len=None, layer: int = 0,
+                 want_scores: bool = False, stream=None):
+    """Pages for each token by the K-min/K-max bound of their keys. Returns a dict: kv_idx [slots,
+    Hkv, T, k], kv_cnt [slots, Hkv, T], scores [slots, Hkv, T, max_pages] (None unless
+    want_scores), dev_status."""
+    Hq, T, qp = _query(q, cache)
+    H = cache.k.shape[2]
+    ql = _qlen(cache, q_len)
+    _, _, b = cache._layer(layer)
+    if b is None:
+        _bad("the cache has no bounds")
+    shape = cache.shape()
+    params = PageSelectParams(cfg.k, cfg.n_first, cfg.n_last)
+    dev = cache.device
+    with _on(dev, stream) as s:
+        nb = lib().bsa_select_pages_workspace_bytes(ctypes.byref(shape), cache.slots, cache.max_pages, Hq, T)
+        if nb == 0:
+            _bad(lib().bsa_last_error().decode(), BSA_ERR_UNSUPPORTED)
+        if not 1 <= cfg.k <= cache.max_pages:
+            _bad("k must be 1..max_pages")
+        r = dict(kv_idx=torch.empty(cache.slots, H, T, cfg.k, dtype=torch.int32, device=dev),
+                 kv_cnt=torch.empty(cache.slots, H, T, dtype=torch.int32, device=dev),
+                 scores=(torch.empty(cache.slots, H, T, cache.max_pages, dtype=torch.float32, device=dev)
+                         if want_scores else None),
+                 dev_status=_status(dev))
+        ws = None if want_scores else _empty_bytes(nb, dev)
+        _check(lib().bsa_select_pages(ctypes.byref(shape), ctypes.byref(params), cache.slots, cache.max_pages,
+                                      Hq, T, qp, b, cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
+                                      r["kv_idx"].data_ptr(), r["kv_cnt"].data_ptr(),
+                                      r["scores"].data_ptr() if want_scores else None,
+                                      r["dev_status"].data_ptr(), ws.data_ptr() if ws is not None else None,
+                                      nb, s))
+    return r

@@ -63,10 +63,12 @@ enum {
   BSA_DEV_OK = 0,
   BSA_DEV_BAD_INDEX = 1,     /* kv_idx entry >= n_kb, > J_t, or a count > W */
   BSA_DEV_TIMEOUT = 2,       /* a bounded wait on an mbarrier ran out */
-  BSA_DEV_BAD_SCORE = 4      /* a candidate block score was NaN or infinite */
+  BSA_DEV_BAD_SCORE = 4,     /* a candidate block score was NaN or infinite */
+  BSA_DEV_NO_PAGES = 8       /* bsa_pages_resize: not enough free pages for every slot */
 };
 
-typedef enum { BSA_BF16 = 0, BSA_F32 = 1 } bsa_dtype;
+/* BSA_F16: the paged-cache calls only. */
+typedef enum { BSA_BF16 = 0, BSA_F32 = 1, BSA_F16 = 2 } bsa_dtype;
 
 /* Block score backbone.
  *   BSA_SCORE_MEAN        s(t,j) = max over the tile's rows i of q_i . mean(K block j)
@@ -335,6 +337,145 @@ bsa_status bsa_select_noalloc(const bsa_shape* shape, const bsa_select_params* p
                               const float* scores, int32_t* kv_idx, int32_t* kv_cnt,
                               float* sigma, float* sigma_bar, uint8_t* trigger, float* theta,
                               int32_t* dev_status, void* stream);
+
+/* ---- paged cache ---------------------------------------------------------------------- */
+
+/* The pages' operations assume one contiguous cache per sequence; the calls below serve many
+ * sequences of different lengths from one pool of pages, with several query tokens a step.
+ *   Pools      k_pages, v_pages [n_pages,Hkv,page,d]; bounds [n_pages,Hkv,2,d], the minimum
+ *              and the maximum over a page's filled rows of each channel of K, of the same type
+ *              ([UGS] Metodologia step 1: the K-min/K-max backbone). One set per layer.
+ *   Table      page_table [slots,max_pages] int32: page p of slot s holds its positions
+ *              [p*page, (p+1)*page); -1 where there is no page. seq_len [slots] int32. refs
+ *              [n_pages] int32: how many table entries name the page; 0 means free. One set for
+ *              all layers. An empty cache is page_table = -1, seq_len = 0, refs = 0.
+ *   Tokens     a call's tokens of slot s are the last q_len[s] positions of it: base =
+ *              seq_len[s] - q_len[s], token t at position base + t. q_len [slots] int32, 0 for a
+ *              slot that takes no part; NULL: T tokens for every slot. Tensors with a token
+ *              axis are padded to T; rows t >= q_len[s] are neither read nor written.
+ *   Types      BSA_BF16 or BSA_F16; d in {64,128}; page in {16,32,64,128}.
+ *   Limits     n_pages*Hkv*page < 2^31, slots <= 4096, max_pages <= 32768, max_pages*page < 2^31,
+ *              T <= 1024 (else BSA_ERR_UNSUPPORTED).
+ *   Errors     a slot whose lengths do not fit (q_len outside 0..T, seq_len < q_len, seq_len >
+ *              max_pages*page) is left out, and a table entry that names no page is not followed;
+ *              both are reported as BSA_DEV_BAD_INDEX in *dev_status (device int32, required).
+ * Calls on one cache run in stream order; the caller orders calls on different streams. */
+typedef struct {
+  int n_pages, Hkv, page, d;
+  bsa_dtype dtype;
+} bsa_cache_shape;
+
+/* Fork: slot c with parent[c] >= 0 becomes a copy of slot parent[c]: its table row and length,
+ * every page gaining a reference. parent [slots] int32, negative for slots left as they are.
+ * Several slots may name one parent. Slot c must be empty (seq_len 0) and its parent must not be
+ * forked in the same call; else c is left as it was (BSA_DEV_BAD_INDEX). */
+bsa_status bsa_pages_fork(int slots, int max_pages, int n_pages, int page, int32_t* page_table,
+                          int32_t* seq_len, int32_t* refs, const int32_t* parent,
+                          int32_t* dev_status, void* stream);
+
+/* Resize: slot s gets the length new_len[s] (negative: left as it is; 0 frees all its pages).
+ * Slots that shrink give up the pages past their new length (a reference each; a page whose count
+ * falls to 0 is free). Then, in slot order, slots that grow take the lowest-numbered free pages: one
+ * for the page that holds their last rows if other slots hold it too (the slot gets a page of its own, and
+ * pairs[s] = (old, new) for bsa_pages_copy), then the pages of their new positions. When all
+ * holders of such a shared page grow in one call, the last of them keeps it.
+ * If there are not enough free pages, the slots (in slot order) from the first that does not fit on
+ * keep their length if they need any (BSA_DEV_NO_PAGES).
+ *   pairs  [slots,2] int32: (-1,-1) where nothing is to be copied. Copy every layer before the
+ *          tokens are appended and before the next resize.
+ *   n_free device int32 or NULL: free pages left.
+ *   refs needs 16-byte alignment. */
+bsa_status bsa_pages_resize(int slots, int max_pages, int n_pages, int page, int32_t* page_table,
+                            int32_t* seq_len, int32_t* refs, const int32_t* new_len, int32_t* pairs,
+                            int32_t* n_free, int32_t* dev_status, void* stream);
+
+/* Copies K, V and bounds (NULL: none) of page pairs[i][0] to page pairs[i][1], pairs [n_pairs,2]
+ * int32 on the device (8-byte aligned); (-1,-1) is skipped. A pair out of range, one whose
+ * destination is the source of any pair, and one whose destination an earlier pair names are
+ * skipped with BSA_DEV_BAD_INDEX. One page may be the source of many pairs. */
+bsa_status bsa_pages_copy(const bsa_cache_shape* shape, void* k_pages, void* v_pages, void* bounds,
+                          const int32_t* pairs, int n_pairs, int32_t* dev_status, void* stream);
+
+/* Append: writes k_new, v_new [slots,Hkv,T,d] to the positions of the call's tokens (seq_len
+ * already counts them: resize comes first) and extends the bounds (NULL: none) of the pages they
+ * fall in; a page whose first row is among them starts afresh. No two slots may append to one
+ * page (resize gives each its own). */
+bsa_status bsa_cache_append(const bsa_cache_shape* shape, int slots, int max_pages, int T,
+                            const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                            void* bounds, const int32_t* page_table, const int32_t* seq_len,
+                            const int32_t* q_len, int32_t* dev_status, void* stream);
+
+/* Compact: of the call's tokens, keeps those of keep [slots,T] int32 (the first n_keep[s] entries,
+ * ascending, in 0..q_len[s]-1): row base + keep[s][i] moves to base + i, in K and V, and the bounds
+ * (NULL: none) of the pages from that of base to that of base + n_keep[s] - 1 are recomputed over the
+ * rows kept. Lengths are not changed: resize to base + n_keep[s] afterwards (it frees the pages
+ * behind). A slot with a bad list is left as it was (BSA_DEV_BAD_INDEX). */
+bsa_status bsa_cache_compact(const bsa_cache_shape* shape, int slots, int max_pages, int T,
+                             const int32_t* keep, const int32_t* n_keep, void* k_pages, void* v_pages,
+                             void* bounds, const int32_t* page_table, const int32_t* seq_len,
+                             const int32_t* q_len, int32_t* dev_status, void* stream);
+
+/* Ancestor masks of trees of drafted tokens: parents [B,T] int32, -1 for a root, parents[t] < t.
+ * mask [B,T,ceil(T/64)] uint64: bit j % 64 of word j / 64 of row t is set when j is t or an
+ * ancestor of t; rows t >= q_len[b] are 0. A parent that does not come before its token counts
+ * as -1 (BSA_DEV_BAD_INDEX). T <= 1024. */
+bsa_status bsa_tree_mask(int B, int T, const int32_t* parents, const int32_t* q_len, uint64_t* mask,
+                         int32_t* dev_status, void* stream);
+
+/* Attention of the call's tokens over the whole cache of their slot: q [slots,Hq,T,d]. Token t sees
+ * every position before base, and position base + j where bit j of its mask row is set (mask as
+ * written by bsa_tree_mask, or any other; NULL: j <= t, a chain). With T = 1 it is plain decode.
+ *   O = sum softmax(scale * q.k) v over the positions seen; out like q, of the cache's type; lse
+ *   [slots,Hq,T] fp32 or NULL, the natural log of the softmax denominator. A token that sees nothing
+ *   gets 0 and -inf. K and V rows that a token does not see do not touch its result, whatever they
+ *   hold (NaN and infinities included).
+ *   Hq a multiple of Hkv, Hq/Hkv <= 16. The workspace (bsa_attend_paged_workspace_bytes, 256-byte
+ *   aligned) need not be initialised; concurrent calls need one each. */
+bsa_status bsa_attend_tree(const bsa_cache_shape* shape, int slots, int max_pages, int Hq, int T,
+                           const void* q, const void* k_pages, const void* v_pages,
+                           const int32_t* page_table, const int32_t* seq_len, const int32_t* q_len,
+                           const uint64_t* mask, float softmax_scale, void* out, float* lse,
+                           int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of bsa_attend_tree and bsa_attend_pages (0 on invalid arguments). */
+size_t bsa_attend_paged_workspace_bytes(const bsa_cache_shape* shape, int slots, int max_pages, int Hq,
+                                        int T);
+
+/* Selection of pages for each token by their key bounds ([UGS] steps 1-2 with the tile being the
+ * query heads of one KV head): s(t,j) = max over the group's heads of
+ * sum_c max(q_c kmin_jc, q_c kmax_jc), the sum in fp64 (the products of 16-bit values are exact),
+ * rounded to fp32. Of the pages 0..J up to the token's own page J = (base+t)/page, the first n_first and
+ * the last n_last are kept; the rest are ranked by (score desc, index asc) up to k pages in all.
+ *   kv_idx [slots,Hkv,T,k] int32: page numbers within the sequence, ascending, -1 padded.
+ *   kv_cnt [slots,Hkv,T] int32. Rows of tokens t >= q_len get -1 and 0.
+ *   scores [slots,Hkv,T,max_pages] fp32 or NULL: s(t,j) for every j <= J, -inf beyond and for tokens
+ *          t >= q_len. NULL: they pass through the workspace.
+ *   n_first >= 0, n_last >= 1, n_first + n_last <= k <= max_pages.
+ *   A ranked page whose score is not finite is reported as BSA_DEV_BAD_SCORE and ranks last (a score
+ *   with an infinite or NaN operand is NaN), as does a page number that the table does not hold
+ *   (BSA_DEV_BAD_INDEX).
+ *   q as in bsa_attend_tree; workspace 256-byte aligned, not initialised. */
+typedef struct {
+  int k, n_first, n_last;
+} bsa_page_select_params;
+size_t bsa_select_pages_workspace_bytes(const bsa_cache_shape* shape, int slots, int max_pages, int Hq,
+                                        int T);
+bsa_status bsa_select_pages(const bsa_cache_shape* shape, const bsa_page_select_params* params, int slots,
+                            int max_pages, int Hq, int T, const void* q, const void* bounds,
+                            const int32_t* page_table, const int32_t* seq_len, const int32_t* q_len,
+                            int32_t* kv_idx, int32_t* kv_cnt, float* scores, int32_t* dev_status,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention of each token over the listed pages: kv_idx [slots,Hkv,T,W], kv_cnt [slots,Hkv,T] as
+ * written by bsa_select_pages (or any other lists; each page listed once). Token t sees the
+ * positions <= base + t of its pages. An entry outside 0..J is skipped and a count outside 0..W
+ * clamped (BSA_DEV_BAD_INDEX). W >= 1. Other arguments and results as bsa_attend_tree. */
+bsa_status bsa_attend_pages(const bsa_cache_shape* shape, int slots, int max_pages, int Hq, int T,
+                            const void* q, const void* k_pages, const void* v_pages,
+                            const int32_t* page_table, const int32_t* seq_len, const int32_t* q_len,
+                            const int32_t* kv_idx, const int32_t* kv_cnt, int W, float softmax_scale,
+                            void* out, float* lse, int32_t* dev_status, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 /* ---- self-test of the bounded device waits ------------------------------------------ */
 
