@@ -92,14 +92,17 @@ struct AttendWs {
   int32_t* part_flag;
   int32_t* cta_status;
   int n_cta;
+  bool tc;
   size_t bytes;
 };
 
-// Sized for the larger of the two calls (lists have the rows of one token).
-AttendWs attend_ws(const bsa_cache_shape& s, int Hq, int T, void* base) {
+AttendWs attend_ws(const bsa_cache_shape& s, int Hq, int T, bool list, void* base) {
   AttendWs w{};
-  w.n_cta = bsa::sm_count();
-  const int rt = (Hq / s.Hkv) * T <= 8 ? 8 : 16;
+  const int rows = (Hq / s.Hkv) * (list ? 1 : T);
+  const bool tc = rows > bsa::kMaxMmaRows;
+  const int rt = tc ? 128 : (rows <= 8 ? 8 : 16);
+  w.n_cta = bsa::sm_count() * (tc ? 2 : 1);
+  w.tc = tc;
   const size_t slots = 2 * (size_t)w.n_cta;
   char* p = (char*)base;
   size_t off = 0;
@@ -123,7 +126,7 @@ bsa_status attend(const bsa_cache_shape* s, int slots, int max_pages, int Hq, in
   if (!aligned(ws, 256)) return fail(BSA_ERR_INVALID_ARG, "workspace needs 256-byte alignment");
   if (mask && !aligned(mask, 8)) return fail(BSA_ERR_INVALID_ARG, "mask needs 8-byte alignment");
   if (!(scale > 0.0f) || !(scale < INFINITY)) return fail(BSA_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
-  AttendWs w = attend_ws(*s, Hq, T, ws);
+  AttendWs w = attend_ws(*s, Hq, T, kv_idx != nullptr, ws);
   if (ws_bytes < w.bytes)
     return fail(BSA_ERR_INVALID_ARG, "workspace too small (%zu < %zu)", ws_bytes, w.bytes);
   bsa::PagedArgs a{};
@@ -146,7 +149,9 @@ bsa_status attend(const bsa_cache_shape* s, int slots, int max_pages, int Hq, in
   a.cta_status = w.cta_status;
   a.dev_status = dev_status;
   a.n_cta = w.n_cta;
-  return done(bsa::launch_paged_attend_mma(*s, a, k, v, (cudaStream_t)stream), "paged attend");
+  cudaStream_t cs = (cudaStream_t)stream;
+  if (w.tc) return done(bsa::launch_paged_attend_tc(*s, a, k, v, cs), "paged attend (tcgen05)");
+  return done(bsa::launch_paged_attend_mma(*s, a, k, v, cs), "paged attend");
 }
 
 }  // namespace
@@ -236,7 +241,9 @@ bsa_status bsa_tree_mask(int B, int T, const int32_t* parents, const int32_t* q_
 
 size_t bsa_attend_paged_workspace_bytes(const bsa_cache_shape* s, int slots, int max_pages, int Hq, int T) {
   if (check_step(s, slots, max_pages, T) != BSA_OK || check_heads(s, slots, Hq, T) != BSA_OK) return 0;
-  return attend_ws(*s, Hq, T, nullptr).bytes;
+  // the larger of the two calls
+  const size_t tree = attend_ws(*s, Hq, T, false, nullptr).bytes, list = attend_ws(*s, Hq, T, true, nullptr).bytes;
+  return tree > list ? tree : list;
 }
 
 bsa_status bsa_attend_tree(const bsa_cache_shape* s, int slots, int max_pages, int Hq, int T, const void* q,

@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
 
 template <int RT, bool F16, bool LIST>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedArgs a) {
-  constexpr float kShift = F16 ? 14.f : 0.f;
+  constexpr float kShift = F16 ? (RT == 128 ? 7.f : 14.f) : 0.f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (c == 0 && blockIdx.y == 0 && warp == 0) {
@@ -521,49 +521,49 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const long long xs = it.first, xe = it.first + it.n_tiles;
   if (xs == x0 || xe > x1) return;               // starts here, or ends later
   if (LIST && it.t >= it.ql) return;
-  const int r = blockIdx.y * 4 + warp;
-  if (r >= it.rows) return;
   int c0 = (int)(xs * w.n_cta / w.total);
   while (c0 > 0 && w.start(c0) > xs) --c0;
   while (w.start(c0 + 1) <= xs) ++c0;
-  // maximum and flags over the parts (c0: slot 1, the others: slot 0; none of them is empty
-  // between the item's first tile and this CTA's)
-  float mx = -INFINITY;
-  int flag = 0;
-  for (int i = c0 + lane; i <= c; i += 32) {
-    const int slot = 2 * i + (i == c0 ? 1 : 0);
-    mx = fmaxf(mx, a.part_ml[((size_t)slot * RT + r) * 2]);
-    flag |= a.part_flag[slot];
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  flag = __reduce_or_sync(0xffffffffu, flag);
   const int d = a.g.d;
-  float ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int r = blockIdx.y * 4 + warp; r < it.rows; r += 4 * gridDim.y) {
+    // maximum and flags over the parts (c0: slot 1, the others: slot 0; none of them is empty
+    // between the item's first tile and this CTA's)
+    float mx = -INFINITY;
+    int flag = 0;
+    for (int i = c0 + lane; i <= c; i += 32) {
+      const size_t slot = 2 * (size_t)i + (i == c0 ? 1 : 0);
+      mx = fmaxf(mx, a.part_ml[(slot * RT + r) * 2]);
+      flag |= a.part_flag[slot];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    flag = __reduce_or_sync(0xffffffffu, flag);
+    float ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int i = c0; i <= c; ++i) {
-    const int slot = 2 * i + (i == c0 ? 1 : 0);
-    const size_t row = (size_t)slot * RT + r;
-    const float m = a.part_ml[row * 2], l = a.part_ml[row * 2 + 1];
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mx);
-    ls += l * f;
-    const float* po = a.part_o + row * d;
+    for (int i = c0; i <= c; ++i) {
+      const size_t slot = 2 * (size_t)i + (i == c0 ? 1 : 0);
+      const size_t row = slot * RT + r;
+      const float m = a.part_ml[row * 2], l = a.part_ml[row * 2 + 1];
+      const float f = m == -INFINITY ? 0.f : exp2f(m - mx);
+      ls += l * f;
+      const float* po = a.part_o + row * d;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (lane + 32 * u < d) acc[u] += po[lane + 32 * u] * f;
-  }
-  int head, t;
-  row_of<LIST>(a, it, r, head, t);
-  const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
-  const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      for (int u = 0; u < 4; ++u)
+        if (lane + 32 * u < d) acc[u] += po[lane + 32 * u] * f;
+    }
+    int head, t;
+    row_of<LIST>(a, it, r, head, t);
+    const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
+    const float inv = ls == 0.f ? 0.f : 1.f / ls;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    if (lane + 32 * u >= d) continue;
-    float x = acc[u] * inv;
-    if (!LIST && flag) x += nonfinite_drafts<F16>(a, it, t, lane + 32 * u);
-    a.out[row * d + lane + 32 * u] = cvt_16<F16>(x);
+    for (int u = 0; u < 4; ++u) {
+      if (lane + 32 * u >= d) continue;
+      float x = acc[u] * inv;
+      if (!LIST && flag) x += nonfinite_drafts<F16>(a, it, t, lane + 32 * u);
+      a.out[row * d + lane + 32 * u] = cvt_16<F16>(x);
+    }
+    if (lane == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
   }
-  if (lane == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
 }
 
 // ---------------------------------------------------------------------------
@@ -581,7 +581,7 @@ template <int RT, bool F16, bool LIST>
 static cudaError_t join_t(const PagedArgs& a, cudaStream_t st) {
   // launched behind the attention kernel without waiting for its end; the kernel itself waits
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.n_cta, RT / 4);
+  cfg.gridDim = dim3(a.n_cta, RT <= 16 ? RT / 4 : 8);
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -599,6 +599,7 @@ static cudaError_t join_rt(const PagedArgs& a, bool list, bool f16, cudaStream_t
 }
 
 cudaError_t launch_paged_join(const PagedArgs& a, int rt, bool list, bool f16, cudaStream_t st) {
+  if (rt == 128) return f16 ? join_t<128, true, false>(a, st) : join_t<128, false, false>(a, st);
   return rt == 8 ? join_rt<8>(a, list, f16, st) : join_rt<16>(a, list, f16, st);
 }
 

@@ -251,13 +251,20 @@ __device__ __noinline__ float nonfinite_drafts(const PagedArgs& a, const Item& i
   return s;
 }
 
-// Joins the partial results of the items that are split over CTAs (rows of RT; grid: n_cta x
-// RT / 4, 128 threads, a warp per row), and gathers the status words.
+// Joins the partial results of the items that are split over CTAs (a warp per row), and gathers
+// the status words. The scale of fp16 weights cancels, but for the lse: shift is its exponent.
 cudaError_t launch_paged_join(const PagedArgs& a, int rt, bool list, bool f16, cudaStream_t st);
 
 // Attention on warp-level MMAs (row tiles of 8 or 16).
 cudaError_t launch_paged_attend_mma(const bsa_cache_shape& s, PagedArgs a, const void* k, const void* v,
                                     cudaStream_t st);
+
+// The same on tcgen05 (row tiles of 128, whole cache only; a.n_cta: two per SM).
+cudaError_t launch_paged_attend_tc(const bsa_cache_shape& s, const PagedArgs& a, const void* k, const void* v,
+                                   cudaStream_t st);
+
+// Query rows per KV head up to which a call runs on warp-level MMAs.
+constexpr int kMaxMmaRows = 16;
 
 int sm_count();
 

@@ -96,10 +96,12 @@ class PagedCache:
         return CacheShape(P, H, page, d, _DTYPES[self.k.dtype])
 
     def _layer(self, layer: int):
-        if not 0 <= layer < self.k.shape[0]:
-            _bad(f"layer {layer} of {self.k.shape[0]}")
-        return (self.k[layer].data_ptr(), self.v[layer].data_ptr(),
-                self.bounds[layer].data_ptr() if self.bounds is not None else None)
+        L, P, H, page, d = self.k.shape
+        if not 0 <= layer < L:
+            _bad(f"layer {layer} of {L}")
+        step = layer * P * H * d * 2
+        return (self.k.data_ptr() + step * page, self.v.data_ptr() + step * page,
+                self.bounds.data_ptr() + 2 * step if self.bounds is not None else None)
 
     def _table(self):
         return self.slots, self.max_pages, self.k.shape[1], self.k.shape[3]
@@ -114,33 +116,47 @@ class PageSelectConfig:
 
 
 def _tensor(name: str, t, shape, dtype, device):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         _bad(f"{name} must be a tensor")
     if t.device != device:
         _bad(f"{name} is on {t.device}, the cache on {device}")
     if t.dtype != dtype:
         _bad(f"{name} must be {dtype}, is {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         _bad(f"{name} must be {list(shape)}, is {list(t.shape)}")
-    if not t.is_contiguous():
-        _bad(f"{name} must be contiguous")
-    return t.data_ptr()
+    _bad(f"{name} must be contiguous")
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Run on the device, outputs and workspaces allocated for the stream that uses them. Yields
-    the stream's handle."""
-    if device.type != "cuda":
-        _bad(f"the cache is on {device}; the kernels need a GPU")
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream)
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+class _On:
+    """Run on the device, outputs and workspaces allocated for the stream that uses them; gives
+    the stream's handle. A step makes several of these calls per layer, so the usual case (the
+    current device and stream) takes no context switch."""
+    __slots__ = ("device", "stream", "inner")
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            _bad(f"the cache is on {device}; the kernels need a GPU")
+        self.device, self.stream, self.inner = device, stream, None
+
+    def __enter__(self):
+        idx = self.device.index
+        if self.stream is None and torch._C._cuda_getDevice() == idx:
+            return torch._C._cuda_getCurrentRawStream(idx)
+        self.inner = contextlib.ExitStack()
+        self.inner.enter_context(torch.cuda.device(self.device))
+        if self.stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        st = torch.cuda.ExternalStream(self.stream) if isinstance(self.stream, int) else self.stream
+        self.inner.enter_context(torch.cuda.stream(st))
+        return st.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.close()
+        return False
 
 
 def _status(device):
@@ -155,7 +171,7 @@ def fork(cache: PagedCache, parent: torch.Tensor, *, stream=None) -> torch.Tenso
     """Slots c with parent[c] >= 0 (int32 [slots]) become copies of their parents, sharing their
     pages. Returns the status."""
     p = _tensor("parent", parent, (cache.slots,), torch.int32, cache.device)
-    with _on(cache.device, stream) as s:
+    with _On(cache.device, stream) as s:
         st = _status(cache.device)
         _check(lib().bsa_pages_fork(*cache._table(), cache.page_table.data_ptr(), cache.seq_len.data_ptr(),
                                     cache.refs.data_ptr(), p, st.data_ptr(), s))
@@ -166,7 +182,7 @@ def resize(cache: PagedCache, new_len: torch.Tensor, *, stream=None):
     """Sets the slots' lengths (int32 [slots]; negative: as it is, 0: freed), taking and giving up
     pages. Returns (pairs [slots, 2] for copy_pages, free pages left, status)."""
     n = _tensor("new_len", new_len, (cache.slots,), torch.int32, cache.device)
-    with _on(cache.device, stream) as s:
+    with _On(cache.device, stream) as s:
         st, n_free = _status(cache.device), _status(cache.device)
         pairs = torch.empty(cache.slots, 2, dtype=torch.int32, device=cache.device)
         _check(lib().bsa_pages_resize(*cache._table(), cache.page_table.data_ptr(),
@@ -183,7 +199,7 @@ def copy_pages(cache: PagedCache, pairs: torch.Tensor, *, layer: int = 0, stream
     p = _tensor("pairs", pairs, (pairs.shape[0], 2), torch.int32, cache.device)
     k, v, b = cache._layer(layer)
     shape = cache.shape()
-    with _on(cache.device, stream) as s:
+    with _On(cache.device, stream) as s:
         st = _status(cache.device)
         if pairs.shape[0] == 0:
             return st.zero_()
@@ -204,7 +220,7 @@ def append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, *, q_len
     ql = _qlen(cache, q_len)
     k, v, b = cache._layer(layer)
     shape = cache.shape()
-    with _on(cache.device, stream) as s:
+    with _On(cache.device, stream) as s:
         st = _status(cache.device)
         _check(lib().bsa_cache_append(ctypes.byref(shape), cache.slots, cache.max_pages, T, kn, vn, k, v, b,
                                       cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
@@ -224,7 +240,7 @@ def compact(cache: PagedCache, keep: torch.Tensor, n_keep: torch.Tensor, *, q_le
     ql = _qlen(cache, q_len)
     k, v, b = cache._layer(layer)
     shape = cache.shape()
-    with _on(cache.device, stream) as s:
+    with _On(cache.device, stream) as s:
         st = _status(cache.device)
         _check(lib().bsa_cache_compact(ctypes.byref(shape), cache.slots, cache.max_pages, T, kp, nk, k, v, b,
                                        cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
@@ -241,7 +257,7 @@ def tree_mask(parents: torch.Tensor, *, q_len=None, stream=None):
     dev = parents.device
     p = _tensor("parents", parents, (B, T), torch.int32, dev)
     ql = None if q_len is None else _tensor("q_len", q_len, (B,), torch.int32, dev)
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         st = _status(dev)
         mask = torch.empty(B, T, (T + 63) // 64, dtype=torch.int64, device=dev)
         _check(lib().bsa_tree_mask(B, T, p, ql, mask.data_ptr(), st.data_ptr(), s))
@@ -266,7 +282,7 @@ def _attend(name, q, cache, extra, q_len, layer, scale, out, lse, stream):
     if lse is not None:
         _tensor("lse", lse, q.shape[:3], torch.float32, cache.device)
     shape = cache.shape()
-    with _on(cache.device, stream) as s:
+    with _On(cache.device, stream) as s:
         st = _status(cache.device)
         # rows past q_len are not written: 0 and -inf in tensors made here
         if out is None:
@@ -324,7 +340,7 @@ def select_pages(q: torch.Tensor, cache: PagedCache, cfg: PageSelectConfig, *, q
     shape = cache.shape()
     params = PageSelectParams(cfg.k, cfg.n_first, cfg.n_last)
     dev = cache.device
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         nb = lib().bsa_select_pages_workspace_bytes(ctypes.byref(shape), cache.slots, cache.max_pages, Hq, T)
         if nb == 0:
             _bad(lib().bsa_last_error().decode(), BSA_ERR_UNSUPPORTED)
