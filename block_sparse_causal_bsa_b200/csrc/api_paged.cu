@@ -114,6 +114,22 @@ AttendWs attend_ws(const bsa_cache_shape& s, int Hq, int T, bool list, void* bas
   return w;
 }
 
+struct SelectWs {
+  float* scores;                     // [slots*Hkv*T][max_pages]
+  float* kmax_abs;                   // [slots*Hkv][max_pages]
+  size_t bytes;
+};
+
+SelectWs select_ws(const bsa_cache_shape& s, int slots, int max_pages, int T, void* base) {
+  SelectWs w{};
+  char* p = (char*)base;
+  size_t off = 0;
+  w.scores = (float*)(p + off); off += align256((size_t)slots * s.Hkv * T * max_pages * 4);
+  w.kmax_abs = (float*)(p + off); off += align256((size_t)slots * s.Hkv * max_pages * 4);
+  w.bytes = off;
+  return w;
+}
+
 bsa_status attend(const bsa_cache_shape* s, int slots, int max_pages, int Hq, int T, const void* q,
                   const void* k, const void* v, const int32_t* table, const int32_t* seq_len,
                   const int32_t* q_len, const uint64_t* mask, const int32_t* kv_idx, const int32_t* kv_cnt,
@@ -273,7 +289,7 @@ bsa_status bsa_attend_pages(const bsa_cache_shape* s, int slots, int max_pages, 
 
 size_t bsa_select_pages_workspace_bytes(const bsa_cache_shape* s, int slots, int max_pages, int Hq, int T) {
   if (check_step(s, slots, max_pages, T) != BSA_OK || check_heads(s, slots, Hq, T) != BSA_OK) return 0;
-  return align256((size_t)slots * s->Hkv * T * max_pages * 4);
+  return select_ws(*s, slots, max_pages, T, nullptr).bytes;
 }
 
 bsa_status bsa_select_pages(const bsa_cache_shape* s, const bsa_page_select_params* p, int slots, int max_pages,
@@ -289,18 +305,17 @@ bsa_status bsa_select_pages(const bsa_cache_shape* s, const bsa_page_select_para
   if (!q || !bounds || !page_table || !seq_len || !kv_idx || !kv_cnt || !dev_status)
     return fail(BSA_ERR_INVALID_ARG, "NULL q, bounds, page_table, seq_len, kv_idx, kv_cnt or dev_status");
   if (!aligned(q, 16) || !aligned(bounds, 16)) return fail(BSA_ERR_INVALID_ARG, "q and bounds need 16-byte alignment");
-  if ((long long)slots * s->Hkv * T * ((max_pages + 127) / 128) >= (1ll << 31))
-    return fail(BSA_ERR_UNSUPPORTED, "slots * Hkv * T * max_pages / 128 must be below 2^31");
-  float* sc = scores;
-  if (!sc) {
+  if ((long long)slots * s->Hkv * T * ((max_pages + 7) / 8) >= (1ll << 31))
+    return fail(BSA_ERR_UNSUPPORTED, "slots * Hkv * T * max_pages / 8 must be below 2^31");
+  SelectWs w{};
+  if (!scores) {
     if (!ws) return fail(BSA_ERR_INVALID_ARG, "NULL workspace without scores");
     if (!aligned(ws, 256)) return fail(BSA_ERR_INVALID_ARG, "workspace needs 256-byte alignment");
-    const size_t need = align256((size_t)slots * s->Hkv * T * max_pages * 4);
-    if (ws_bytes < need) return fail(BSA_ERR_INVALID_ARG, "workspace too small (%zu < %zu)", ws_bytes, need);
-    sc = (float*)ws;
+    w = select_ws(*s, slots, max_pages, T, ws);
+    if (ws_bytes < w.bytes) return fail(BSA_ERR_INVALID_ARG, "workspace too small (%zu < %zu)", ws_bytes, w.bytes);
   }
   return done(bsa::launch_select_pages(*s, geom(s, slots, max_pages, T, page_table, seq_len, q_len), *p, Hq, q,
-                                       bounds, sc, scores != nullptr, kv_idx, kv_cnt, dev_status,
+                                       bounds, scores ? scores : w.scores, w.kmax_abs, kv_idx, kv_cnt, dev_status,
                                        (cudaStream_t)stream), "select pages");
 }
 

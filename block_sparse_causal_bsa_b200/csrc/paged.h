@@ -58,10 +58,13 @@ cudaError_t launch_tree_mask(int B, int T, const int32_t* parents, const int32_t
 
 namespace bsa {
 
-// Page scores into scores [slots*Hkv*T][max_pages], then the lists. fill: write -inf past the
-// visible pages too.
+int sm_count();                        // of the current device
+
+// Page scores into scores [slots*Hkv*T][max_pages], then the lists. kmax_abs [slots*Hkv][max_pages]
+// (workspace): the scores are fp32 estimates, and what they leave open is decided in fp64; null: the
+// scores are exact, -inf past the visible pages.
 cudaError_t launch_select_pages(const bsa_cache_shape& s, const CacheGeom& g, const bsa_page_select_params& p,
-                                int Hq, const void* q, const void* bounds, float* scores, bool fill,
+                                int Hq, const void* q, const void* bounds, float* scores, float* kmax_abs,
                                 int32_t* kv_idx, int32_t* kv_cnt, int32_t* dev_status, cudaStream_t st);
 
 }  // namespace bsa

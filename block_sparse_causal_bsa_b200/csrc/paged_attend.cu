@@ -26,6 +26,7 @@
 // Rows that are no keys (the tail of the last page, missing pages) have their S masked and their
 // V rows zeroed in shared memory, and non-finite values of drafted tokens are taken out of the
 // tile and given back only to rows that see them.
+#include <limits.h>
 #include <math.h>
 
 #include "paged_work.cuh"
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl<D, RT>& c = *reinterpret_cast<Ctrl<D, RT>*>(sm + C::kStages * C::kStage);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
 
   Walk<LIST, RT> w;
   w.init(a);
-  const long long x0 = w.start(blockIdx.x), x1 = blockIdx.x < w.n_cta ? w.start(blockIdx.x + 1) : x0;
+  const long long x0 = w.start(blockIdx.x), x1 = w.start(blockIdx.x + 1);
   int tiles_issued = 0;
 
   if (warp == 0) {
@@ -150,36 +152,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
       const int32_t* table = a.g.table + (size_t)it.b * a.g.max_pages;
       const int32_t* list = LIST ? a.kv_idx + (((size_t)it.b * a.g.Hkv + it.h) * a.g.T + it.t) * a.W : nullptr;
       const int limit = LIST ? it.base + it.t + 1 : it.base + it.ql;     // positions below it are keys
-      // lane i: box (i % npt) of tile t0 + i / npt
+      // Lane i: box (i % npt) of tile t0 + i / npt. The table entries of the batch after this one and
+      // the list entries of the one after that are on their way while a batch is issued.
       const int per_load = 32 / npt;
-      for (int t0 = ta; ok && t0 < tb; t0 += per_load) {
+      auto entry = [&](int t0) -> int {          // the box's page number within the sequence, -1: none
         const int tile = t0 + lane / npt;
-        const int slot_row = tile * kTileKeys + (lane % npt) * rpb;      // row in the item's page order
-        const int e = slot_row / page, off = slot_row % page;
+        if (tile >= tb) return -1;
+        const int e = (tile * kTileKeys + (lane % npt) * rpb) / page;
+        if (!LIST) return e * page < limit ? e : -1;
+        return e < cnt ? max(__ldg(list + e), -1) : INT_MIN;
+      };
+      auto held = [&](int j) -> int {            // its page of the pool
+        return j >= 0 && (long long)j * page < limit ? __ldg(table + j) : -1;
+      };
+      int j_now = entry(ta), pg_now = held(j_now), j_next = entry(ta + per_load);
+      for (int t0 = ta; ok && t0 < tb; t0 += per_load) {
+        const int pg_next = held(j_next), j_next2 = entry(t0 + 2 * per_load);
+        const int off = ((t0 + lane / npt) * kTileKeys + (lane % npt) * rpb) % page;
         int rows = 0, y = 0;
-        if (tile < tb) {
-          int j = e;
-          bool in = true;
-          if (LIST) {
-            in = e < cnt;
-            if (in) {
-              j = list[e];
-              if (j < 0 || (long long)j * page >= limit) {
-                bad = true;
-                in = false;
-              }
+        if (LIST ? j_now != INT_MIN && t0 + lane / npt < tb : j_now >= 0) {
+          if (j_now < 0 || (long long)j_now * page >= limit) {
+            bad = true;                          // a list entry past the token's page
+          } else {
+            rows = min(max(limit - (j_now * page + off), 0), rpb);
+            if (rows > 0 && (pg_now < 0 || pg_now >= a.g.n_pages)) {
+              bad = true;
+              rows = 0;
             }
-          }
-          if (in) {
-            rows = min(max(limit - (j * page + off), 0), rpb);
-            if (rows > 0) {
-              const int pg = table[j];
-              if (pg < 0 || pg >= a.g.n_pages) {
-                bad = true;
-                rows = 0;
-              }
-              y = (int)(((long long)pg * a.g.Hkv + it.h) * page) + off;
-            }
+            y = (int)(((long long)pg_now * a.g.Hkv + it.h) * page) + off;
           }
         }
         unsigned long long bits = rows == 0 ? 0 : (rows == 64 ? ~0ull : (1ull << rows) - 1) << ((lane % npt) * rpb);
@@ -209,6 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
           }
           ++n;
         }
+        j_now = j_next;
+        pg_now = pg_next;
+        j_next = j_next2;
       }
       if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&c.status, BSA_DEV_BAD_INDEX);
       x = xe;
@@ -496,11 +499,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
 
 // ---------------------------------------------------------------------------
 
+// Joins the parts of split items: block x does the item that ends in CTA x's share and began in
+// an earlier one, a warp per row. What a row needs of the split is found before the wait for the
+// attention kernel, the weights of the parts sit in the lanes, and the reads of the parts' outputs
+// (16 bytes a lane) do not depend on one another: the kernel is a few memory latencies long.
+constexpr int kJoinWarps = 8;
+
 template <int RT, bool F16, bool LIST>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedArgs a) {
   constexpr float kShift = F16 ? (RT == 128 ? 7.f : 14.f) : 0.f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  Walk<LIST, RT> w;
+  w.init(a);
+  Item it;
+  bool work = false;
+  int c0 = 0;
+  const long long x0 = w.start(c), x1 = w.start(c + 1);
+  if (x0 < x1) {
+    w.locate(a, x0, it);
+    const long long xs = it.first, xe = it.first + it.n_tiles;
+    work = xs < x0 && xe <= x1 && (!LIST || it.t < it.ql);
+    if (work) c0 = w.owner(xs);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c == 0 && blockIdx.y == 0 && warp == 0) {
     int st = 0;
     for (int i = lane; i < a.n_cta; i += 32) st |= a.cta_status[i];
@@ -511,57 +532,73 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     st = __reduce_or_sync(0xffffffffu, st);
     if (lane == 0) *a.dev_status = st;
   }
-  Walk<LIST, RT> w;
-  w.init(a);
-  if (c >= w.n_cta) return;
-  const long long x0 = w.start(c), x1 = w.start(c + 1);
-  if (x0 >= x1) return;
-  Item it;
-  w.locate(a, x0, it);
-  const long long xs = it.first, xe = it.first + it.n_tiles;
-  if (xs == x0 || xe > x1) return;               // starts here, or ends later
-  if (LIST && it.t >= it.ql) return;
-  int c0 = (int)(xs * w.n_cta / w.total);
-  while (c0 > 0 && w.start(c0) > xs) --c0;
-  while (w.start(c0 + 1) <= xs) ++c0;
-  const int d = a.g.d;
-  for (int r = blockIdx.y * 4 + warp; r < it.rows; r += 4 * gridDim.y) {
-    // maximum and flags over the parts (c0: slot 1, the others: slot 0; none of them is empty
-    // between the item's first tile and this CTA's)
+  if (!work) return;
+  const int d = a.g.d, np = c - c0 + 1;          // parts: CTA c0's slot 1, the others' slot 0 (none is empty)
+  const int lpr = d / 4;                         // lanes per row of a part: 32 or 16 (two parts at a time)
+  const int dl = (lane % lpr) * 4, half = lane / lpr, step = 32 / lpr;
+  auto row_of_part = [&](int i, int r) { return (2 * (size_t)(c0 + i) + (i == 0 ? 1 : 0)) * RT + r; };
+  for (int r = blockIdx.y * kJoinWarps + warp; r < it.rows; r += kJoinWarps * gridDim.y) {
+    // lane i: maximum and sum of part i, kept when there are no more than 32 parts
+    float2 ml = make_float2(-INFINITY, 0.f);
     float mx = -INFINITY;
     int flag = 0;
-    for (int i = c0 + lane; i <= c; i += 32) {
-      const size_t slot = 2 * (size_t)i + (i == c0 ? 1 : 0);
-      mx = fmaxf(mx, a.part_ml[(slot * RT + r) * 2]);
-      flag |= a.part_flag[slot];
+    for (int i = lane; i < np; i += 32) {
+      ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row_of_part(i, r) * 2));
+      mx = fmaxf(mx, ml.x);
+      if (!LIST) flag |= __ldcg(a.part_flag + 2 * (c0 + i) + (i == 0 ? 1 : 0));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     flag = __reduce_or_sync(0xffffffffu, flag);
     float ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = c0; i <= c; ++i) {
-      const size_t slot = 2 * (size_t)i + (i == c0 ? 1 : 0);
-      const size_t row = slot * RT + r;
-      const float m = a.part_ml[row * 2], l = a.part_ml[row * 2 + 1];
-      const float f = m == -INFINITY ? 0.f : exp2f(m - mx);
-      ls += l * f;
-      const float* po = a.part_o + row * d;
+    for (int i0 = 0; i0 < np; i0 += 32) {
+      if (np > 32) {
+        ml = make_float2(-INFINITY, 0.f);
+        if (i0 + lane < np) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row_of_part(i0 + lane, r) * 2));
+      }
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mx);      // lane i: weight of part i0 + i
+      ls += ml.y * f;
+      const int n = min(32, np - i0);
+      constexpr int kU = 8;                                            // reads in flight
+      for (int i = 0; i < n; i += kU * step) {
+        float4 v[kU];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (lane + 32 * u < d) acc[u] += po[lane + 32 * u] * f;
+        for (int u = 0; u < kU; ++u) {
+          const int p = i + u * step + half;
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p < n) v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row_of_part(i0 + p, r) * d + dl));
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int p = i + u * step + half;
+          const float fp = __shfl_sync(0xffffffffu, f, p & 31);
+          if (p < n) {
+            acc[0] = fmaf(v[u].x, fp, acc[0]);
+            acc[1] = fmaf(v[u].y, fp, acc[1]);
+            acc[2] = fmaf(v[u].z, fp, acc[2]);
+            acc[3] = fmaf(v[u].w, fp, acc[3]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+    if (lpr == 16) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) acc[u] += __shfl_xor_sync(0xffffffffu, acc[u], 16);
     }
     int head, t;
     row_of<LIST>(a, it, r, head, t);
     const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
     const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    float y[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      if (lane + 32 * u >= d) continue;
-      float x = acc[u] * inv;
-      if (!LIST && flag) x += nonfinite_drafts<F16>(a, it, t, lane + 32 * u);
-      a.out[row * d + lane + 32 * u] = cvt_16<F16>(x);
+      y[u] = acc[u] * inv;
+      if (!LIST && flag) y[u] += nonfinite_drafts<F16>(a, it, t, dl + u);
     }
+    if (half == 0)
+      *reinterpret_cast<uint2*>(a.out + row * d + dl) = make_uint2(pack_16<F16>(y[0], y[1]), pack_16<F16>(y[2], y[3]));
     if (lane == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
   }
 }
@@ -581,8 +618,8 @@ template <int RT, bool F16, bool LIST>
 static cudaError_t join_t(const PagedArgs& a, cudaStream_t st) {
   // launched behind the attention kernel without waiting for its end; the kernel itself waits
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.n_cta, RT <= 16 ? RT / 4 : 8);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(a.n_cta, RT / kJoinWarps);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
   Ctrl& c = *reinterpret_cast<Ctrl*>(sm + C::kCtrl);
   const uint32_t sQ = tc::smem_u32(sm + C::kQ), sK = tc::smem_u32(sm + C::kK), sV = tc::smem_u32(sm + C::kV);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  launch_dependents();
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&c.q_full, 4);
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
 
   Walk<false, RT> w;
   w.init(a);
-  const long long x0 = w.start(blockIdx.x), x1 = blockIdx.x < w.n_cta ? w.start(blockIdx.x + 1) : x0;
+  const long long x0 = w.start(blockIdx.x), x1 = w.start(blockIdx.x + 1);
   Item it;
   if (x0 < x1) w.locate(a, x0, it);
   int k_issued = 0, v_issued = 0;

@@ -20,10 +20,6 @@ namespace bsa {
 
 constexpr int kTileKeys = 64;
 
-// How far a share may shrink: with fewer tiles than this per CTA, the join costs more than the
-// split saves.
-constexpr int kMinTiles = 1;
-
 struct PagedArgs {
   CacheGeom g;
   int Hq, G;                        // query heads, heads per KV head
@@ -60,7 +56,7 @@ struct Item {
 template <bool LIST, int RT>
 struct Walk {
   long long total;                  // tiles of all items
-  int n_cta;                        // CTAs that get a share
+  long long per;                    // tiles per CTA (the last ones may have fewer, or none)
 
   __device__ static int slot_items(const PagedArgs& a, int ql) {
     return a.g.Hkv * ceil_div_i(a.G * ql, RT);
@@ -87,18 +83,22 @@ struct Walk {
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       total = s;
     }
-    const long long n = total / kMinTiles;
-    n_cta = n < 1 ? 1 : (n < a.n_cta ? (int)n : a.n_cta);
+    const long long n = total + a.n_cta - 1;         // (64-bit divisions are slow)
+    per = n >> 32 ? n / a.n_cta : (long long)((uint32_t)n / (uint32_t)a.n_cta);
   }
-  __device__ long long start(int c) const { return c >= n_cta ? total : total * c / n_cta; }
+  __device__ long long start(int c) const { return min(c * per, total); }
+  // the CTA whose share holds tile x
+  __device__ int owner(long long x) const {
+    return x >> 32 || per >> 32 ? (int)(x / per) : (int)((uint32_t)x / (uint32_t)per);
+  }
 
   __device__ void set_list_item(const PagedArgs& a, long long item, Item& it) const {
     it.n_tiles = list_tiles(a);
     it.first = item * it.n_tiles;
-    it.t = (int)(item % a.g.T);
-    const long long bh = item / a.g.T;
-    it.h = (int)(bh % a.g.Hkv);
-    it.b = (int)(bh / a.g.Hkv);
+    it.t = (int)item % a.g.T;                        // (slots * Hq * T is below 2^31)
+    const int bh = (int)item / a.g.T;
+    it.h = bh % a.g.Hkv;
+    it.b = bh / a.g.Hkv;
     query_span(a.g, it.b, it.base, it.ql);
     it.row0 = 0;
     it.rows = a.G;
@@ -118,7 +118,8 @@ struct Walk {
   // The item of tile x (0 <= x < total). Whole warp.
   __device__ void locate(const PagedArgs& a, long long x, Item& it) const {
     if (LIST) {
-      set_list_item(a, x / list_tiles(a), it);
+      const int n = list_tiles(a);
+      set_list_item(a, x >> 32 ? x / n : (long long)((uint32_t)x / (uint32_t)n), it);
       return;
     }
     const int lane = threadIdx.x % 32;
@@ -138,7 +139,9 @@ struct Walk {
         const long long first = before + __shfl_sync(0xffffffffu, p - w, l);
         int base, ql;
         query_span(a.g, b0 + l, base, ql);
-        set_slot_item(a, b0 + l, first, (int)((x - first) / ceil_div_i(base + ql, kTileKeys)), it);
+        const long long off = x - first;
+        const int nt = ceil_div_i(base + ql, kTileKeys);
+        set_slot_item(a, b0 + l, first, off >> 32 ? (int)(off / nt) : (int)((uint32_t)off / (uint32_t)nt), it);
         return;
       }
       before += __shfl_sync(0xffffffffu, p, 31);
@@ -148,7 +151,7 @@ struct Walk {
   __device__ void next(const PagedArgs& a, Item& it) const {
     const long long x = it.first + it.n_tiles;
     if (LIST) {
-      set_list_item(a, x / it.n_tiles, it);
+      set_list_item(a, ((long long)it.b * a.g.Hkv + it.h) * a.g.T + it.t + 1, it);
       return;
     }
     const int mts = ceil_div_i(a.G * it.ql, RT);
@@ -196,6 +199,10 @@ __device__ __forceinline__ bool sees_draft(const PagedArgs& a, int b, int t, int
   if (!a.mask) return j <= t;
   return (a.mask[((size_t)b * a.g.T + t) * a.words + (j >> 6)] >> (j & 63)) & 1ull;
 }
+
+// The kernel launched behind this one (with programmatic serialization) may start its blocks as
+// room appears; it waits for the end of this one itself before it reads results.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <bool F16>
 __device__ __forceinline__ float cvt_f32(uint16_t x) {
@@ -265,7 +272,5 @@ cudaError_t launch_paged_attend_tc(const bsa_cache_shape& s, const PagedArgs& a,
 
 // Query rows per KV head up to which a call runs on warp-level MMAs.
 constexpr int kMaxMmaRows = 16;
-
-int sm_count();
 
 }  // namespace bsa
