@@ -2,6 +2,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <algorithm>
+
 #include "kernels.h"
 #include "paged_work.cuh"
 
@@ -90,7 +92,7 @@ struct AttendWs {
   float* part_o;
   float* part_ml;
   int32_t* part_flag;
-  int32_t* cta_status;
+  int32_t* arrived;
   int n_cta;
   bool tc;
   size_t bytes;
@@ -101,7 +103,7 @@ AttendWs attend_ws(const bsa_cache_shape& s, int Hq, int T, bool list, void* bas
   const int rows = (Hq / s.Hkv) * (list ? 1 : T);
   const bool tc = rows > bsa::kMaxMmaRows;
   const int rt = tc ? 128 : (rows <= 8 ? 8 : 16);
-  w.n_cta = bsa::sm_count() * (tc ? 2 : 1);
+  w.n_cta = tc ? 2 * bsa::sm_count() : std::min(bsa::sm_count(), bsa::kMaxPartsCtas);
   w.tc = tc;
   const size_t slots = 2 * (size_t)w.n_cta;
   char* p = (char*)base;
@@ -109,7 +111,7 @@ AttendWs attend_ws(const bsa_cache_shape& s, int Hq, int T, bool list, void* bas
   w.part_o = (float*)(p + off); off += align256(slots * rt * s.d * 4);
   w.part_ml = (float*)(p + off); off += align256(slots * rt * 2 * 4);
   w.part_flag = (int32_t*)(p + off); off += align256(slots * 4);
-  w.cta_status = (int32_t*)(p + off); off += align256((size_t)w.n_cta * 4);
+  w.arrived = (int32_t*)(p + off); off += align256((size_t)w.n_cta * 4);
   w.bytes = off;
   return w;
 }
@@ -162,7 +164,7 @@ bsa_status attend(const bsa_cache_shape* s, int slots, int max_pages, int Hq, in
   a.part_o = w.part_o;
   a.part_ml = w.part_ml;
   a.part_flag = w.part_flag;
-  a.cta_status = w.cta_status;
+  a.arrived = w.arrived;
   a.dev_status = dev_status;
   a.n_cta = w.n_cta;
   cudaStream_t cs = (cudaStream_t)stream;

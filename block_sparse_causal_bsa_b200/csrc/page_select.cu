@@ -397,15 +397,16 @@ struct Cut {
 };
 
 // Radix selection: digits of up to eight bits from the highest bit in which keys differ down; mn, mx
-// the least and the largest key. All threads call it; keys are visible to all.
-__device__ Cut radix_cut(const uint32_t* keys, int n, int m, unsigned mn, unsigned mx, ListSmem& s) {
+// the least and the largest key; at most `digits` of them (the cut then lies within the last one's
+// range). All threads call it; keys are visible to all.
+__device__ Cut radix_cut(const uint32_t* keys, int n, int m, unsigned mn, unsigned mx, ListSmem& s, int digits) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   Cut c{mx, 0xffffffffu, m};
   if (mn == mx) return c;
   int top = 32 - __clz(mn ^ mx);                // bits [0, top) differ
   c.mask = top == 32 ? 0u : ~((1u << top) - 1u);
   c.thr = mx & c.mask;
-  while (top > 0) {
+  for (; top > 0 && digits > 0; --digits) {
     const int sh = max(top - 8, 0), width = top - sh;
     s.hist[tid] = 0;
     __syncthreads();
@@ -451,20 +452,28 @@ __device__ float exact_score(const uint16_t* bp, const double* qd, int G, int d)
   const uint2 hi = on ? __ldg(reinterpret_cast<const uint2*>(bp + d) + lane) : make_uint2(0, 0);
   const uint32_t kl[4] = {dbl_hi<F16>(lo.x << 16), dbl_hi<F16>(lo.x), dbl_hi<F16>(lo.y << 16), dbl_hi<F16>(lo.y)};
   const uint32_t kh[4] = {dbl_hi<F16>(hi.x << 16), dbl_hi<F16>(hi.x), dbl_hi<F16>(hi.y << 16), dbl_hi<F16>(hi.y)};
-  for (int i = 0; i < G; ++i) {
-    double s = 0.0;
-    if (on) {
+  for (int i0 = 0; i0 < G; i0 += 4) {            // four heads' sums at a time hide their latencies
+    double sum[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const double x = qd[i * d + lane * 4 + c];
-        s = fma(x, __hiloint2double((int)(__double2hiint(x) < 0 ? kl[c] : kh[c]), 0), s);
+    for (int i = 0; i < 4; ++i) {
+      sum[i] = 0.0;
+      if (on) {
+        const double* x = qd + min(i0 + i, G - 1) * d + lane * 4;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          sum[i] = fma(x[c], __hiloint2double((int)(__double2hiint(x[c]) < 0 ? kl[c] : kh[c]), 0), sum[i]);
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float f = (float)s;
-    nan |= f != f;
-    best = fmaxf(best, f);
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = (float)sum[i];
+      nan |= f != f;
+      best = fmaxf(best, f);
+    }
   }
   return nan ? __uint_as_float(kBadScore) : best;
 }
@@ -575,82 +584,76 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
 #pragma unroll
   for (int i = 0; i < kListWarps; ++i) kabs = fmaxf(kabs, s.fred[i]);
   __syncthreads();                              // red is read
-  Cut c = radix_cut(keys, n, m, mn, mx, s);
+  // the screen needs the threshold to within the margin only: two digits, 2^-16 of the keys' range
+  Cut c = radix_cut(keys, n, m, mn, mx, s, SCREEN ? 2 : 4);
 
   if (SCREEN) {
-    // theta: any key of the threshold digit range bounds it from both sides
     const float th_lo = key_score(c.thr), th_hi = key_score(c.thr | ~c.mask);
-    // 2^-14 for the sums; what a 16-bit subnormal could lose if an MMA flushed it; and an ulp
+    // 2^-14 for the sums; what 16-bit subnormals could lose if an MMA flushed them
     const float delta = 0x1p-14f * q1 * kabs + (F16 ? 0x1p-13f : 0x1p-100f) * (q1 + g.d * kabs);
     const float lo = th_lo - 2.f * delta, hi = th_hi + 2.f * delta;
     // (an infinite or NaN margin puts everything but the pages known to be bad, key 0, in the window)
+    const unsigned sure = hi < INFINITY ? score_key(hi) : 0xfffffffeu;      // keys above it are in
     int in = 0;
     for (int i = tid; i < n; i += kListThreads) {
-      const float v = key_score(keys[i]);
-      const bool above = v > hi && v < INFINITY, below = v < lo && keys[i] != 0;
-      in += above;
-      if (!above && !below && keys[i] != 0) {
+      const unsigned key = keys[i];
+      in += key > sure;
+      if (key <= sure && key != 0 && !(key_score(key) < lo)) {
         const int at = atomicAdd(&s.n_win, 1);
         if (at < kWindow) s.win[at] = i;
       }
     }
     in = __reduce_add_sync(0xffffffffu, in);
-    __syncthreads();
-    if (lane == 0) s.red[warp] = in;
+    if (lane == 0) s.red2[warp] = in;
     __syncthreads();
     in = 0;
 #pragma unroll
-    for (int i = 0; i < kListWarps; ++i) in += s.red[i];
+    for (int i = 0; i < kListWarps; ++i) in += s.red2[i];
     const int nw = s.n_win, need = m - in;
-    if (nw > need) {
-      // exact scores of the window, a warp per page. Keys become 0xffffffff (in), 0 (out) or the
-      // exact key between them.
-      if (nw <= kWindow) {
+    const int32_t* table = g.table + (size_t)b * g.max_pages + p.n_first;
+    const uint16_t* bh_bounds = bounds + (size_t)h * 2 * g.d;
+    const size_t page_stride = (size_t)g.Hkv * 2 * g.d;
+    if (nw < need) {
+      c = Cut{0u, 0xffffffffu, need - nw};       // every page that is not bad, and the first bad ones
+    } else if (nw <= kWindow) {
+      c = Cut{sure, 0xffffffffu, 0};
+      if (nw > need) {
+        // exact scores of the window, a warp per page, then ranks within it
         for (int w = warp; w < nw; w += kListWarps) {
-          const int i = s.win[w];
-          const int pg = g.table[(size_t)b * g.max_pages + p.n_first + i];
-          const float e = exact_score<F16>(bounds + ((size_t)pg * g.Hkv + h) * 2 * g.d, s.qd, G, g.d);
+          const float e = exact_score<F16>(bh_bounds + __ldg(table + s.win[w]) * page_stride, s.qd, G, g.d);
           if (lane == 0) {
             if (!(fabsf(e) < INFINITY)) atomicOr(&s.status, BSA_DEV_BAD_SCORE);
             s.wkey[w] = fabsf(e) < INFINITY ? score_key(e) : 0u;
           }
         }
         __syncthreads();
-        for (int i = tid; i < n; i += kListThreads) {
-          const float v = key_score(keys[i]);
-          keys[i] = keys[i] != 0 && v > hi && v < INFINITY ? 0xffffffffu : 0u;
-        }
-        __syncthreads();
-        if (tid < nw) {
-          // the rank among the window decides
-          const uint32_t key = s.wkey[tid];
-          const int i = s.win[tid];
-          int better = 0;
-          for (int w = 0; w < nw; ++w) better += s.wkey[w] > key || (s.wkey[w] == key && s.win[w] < i);
-          if (better < need) keys[i] = 0xffffffffu;
-        }
-        __syncthreads();
-        c = Cut{0x7fffffffu, 0xffffffffu, 0};
-      } else {
-        for (int i0 = warp; i0 < n; i0 += kListWarps) {
-          const uint32_t key = keys[i0];
-          const float v = key_score(key);
-          uint32_t out_key = 0;
-          if (key != 0 && v > hi && v < INFINITY) {
-            out_key = 0xffffffffu;
-          } else if (key != 0 && !(v < lo)) {
-            const int pg = g.table[(size_t)b * g.max_pages + p.n_first + i0];
-            const float e = exact_score<F16>(bounds + ((size_t)pg * g.Hkv + h) * 2 * g.d, s.qd, G, g.d);
-            if (fabsf(e) < INFINITY) out_key = score_key(e);
-            else if (lane == 0) atomicOr(&s.status, BSA_DEV_BAD_SCORE);
-          }
-          __syncwarp();
-          if (lane == 0) keys[i0] = out_key;
-        }
-        __syncthreads();
-        c = radix_cut(keys, n, m, 0u, 0xffffffffu, s);
       }
+      if (tid < nw) {
+        const int i = s.win[tid];
+        int better = 0;
+        if (nw > need) {
+          const uint32_t key = s.wkey[tid];
+          for (int w = 0; w < nw; ++w) better += s.wkey[w] > key || (s.wkey[w] == key && s.win[w] < i);
+        }
+        if (better < need) keys[i] = 0xffffffffu;
+      }
+    } else {
+      // a large window (copies of pages, an unusable margin): its exact keys, and another selection
+      for (int i = warp; i < n; i += kListWarps) {
+        const unsigned key = keys[i];
+        unsigned exact = key > sure ? 0xffffffffu : 0u;
+        if (key <= sure && key != 0 && !(key_score(key) < lo)) {
+          const float e = exact_score<F16>(bh_bounds + __ldg(table + i) * page_stride, s.qd, G, g.d);
+          if (fabsf(e) < INFINITY) exact = score_key(e);
+          else if (lane == 0) atomicOr(&s.status, BSA_DEV_BAD_SCORE);
+        }
+        __syncwarp();
+        if (lane == 0) keys[i] = exact;
+      }
+      __syncthreads();
+      c = radix_cut(keys, n, m, 0u, 0xffffffffu, s, 4);
     }
+    __syncthreads();
   }
   if (tid == 0 && s.status) set_status(dev_status, s.status);
   // in: (key & mask) > thr, or equal and among the first `left` of those. A warp takes a
@@ -684,12 +687,12 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
   }
 }
 
-// Pages per CTA of the scoring kernels: four CTAs per SM over the whole table, in whole steps of their
-// warps. More per CTA would leave SMs idle where sequences are shorter than the table; fewer
-// repeats the load of the queries.
+// Pages per CTA of the scoring kernels, in whole steps of their warps: two CTAs per SM (what fits)
+// over the whole table, so that the load of the queries is paid once.
 int pages_per_cta(long long rows, int max_pages, int step) {
-  const long long per = rows * max_pages / (4ll * sm_count()) / step * step;
-  return (int)(per < step ? step : (per > 65536 ? 65536 : per));
+  const long long ctas = 2ll * sm_count();
+  const long long per = ((rows * max_pages + ctas - 1) / ctas + step - 1) / step * step;
+  return (int)(per > 65536 ? 65536 : per);
 }
 
 template <int D, int G>

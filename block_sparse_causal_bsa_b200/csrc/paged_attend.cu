@@ -75,28 +75,108 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // the eight compute warps
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-template <int D>
+template <int D, int RT>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kHalf = kTileKeys * 128;          // 64 rows x 128 bytes
   static constexpr uint32_t kTile = kHalves * kHalf;          // K or V of a tile
   static constexpr uint32_t kStage = 2 * kTile;
-  static constexpr int kStages = D == 128 ? 6 : 10;
+  static constexpr int kStages = D == 128 ? (RT == 8 ? 6 : 5) : 8;
 };
+
+// Column of channel d in row r of a dumped output: the rows 2 tig of a fragment's store fall eight
+// banks apart, and four neighbouring channels stay together.
+__device__ __forceinline__ int dump_col(int r, int d) { return d ^ (((r >> 1) & 3) << 3); }
 
 template <int D, int RT>
 struct __align__(16) Ctrl {
-  uint64_t full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
-  unsigned long long vmask[Cfg<D>::kStages];    // rows of the stage that are keys of its item
+  uint64_t full[Cfg<D, RT>::kStages], empty[Cfg<D, RT>::kStages];
+  unsigned long long vmask[Cfg<D, RT>::kStages];    // rows of the stage that are keys of its item
   int abort_flag;
   int32_t status;
   int flag[2];                                  // by segment parity: non-finite drafts taken out
+  int last;                                     // this CTA joins the item's parts
   float m[kWarps][RT], l[kWarps][RT];
-  float o[RT][D + 4];
+  union {
+    alignas(16) float o[kWarps][RT][D];      // the warps' unnormalised outputs
+    float2 ml[kWarps * RT * D / 2];             // maxima and sums of an item's parts
+  };
 };
 
 template <int D, int RT>
-constexpr size_t smem_bytes() { return 1024 + Cfg<D>::kStages * Cfg<D>::kStage + sizeof(Ctrl<D, RT>); }
+constexpr size_t smem_bytes() { return 1024 + Cfg<D, RT>::kStages * Cfg<D, RT>::kStage + sizeof(Ctrl<D, RT>); }
+
+// Four values of a row, final: normalised, with the non-finite drafted values, rounded and stored.
+template <int D, bool F16, bool LIST>
+__device__ __forceinline__ void store_row4(const PagedArgs& a, const Item& it, int r, int d4, float4 v, float mx,
+                                           float ls, bool fixup) {
+  constexpr float kShift = F16 ? 14.f : 0.f;
+  int head, t;
+  row_of<LIST>(a, it, r, head, t);
+  const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
+  const float inv = ls == 0.f ? 0.f : 1.f / ls;
+  float y[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+  if (!LIST && fixup) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) y[u] += nonfinite_drafts<F16>(a, it, t, d4 + u);
+  }
+  *reinterpret_cast<uint2*>(a.out + row * D + d4) = make_uint2(pack_16<F16>(y[0], y[1]), pack_16<F16>(y[2], y[3]));
+  if (d4 == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
+}
+
+__device__ __forceinline__ void add4(float4& acc, const float4& v, float f) {
+  acc.x = fmaf(v.x, f, acc.x);
+  acc.y = fmaf(v.y, f, acc.y);
+  acc.z = fmaf(v.z, f, acc.z);
+  acc.w = fmaf(v.w, f, acc.w);
+}
+
+// Joins the parts of an item, the 256 threads of the compute warps: four values of a row each, the
+// first reads of the parts' outputs on their way with those of their maxima and sums.
+template <int D, int RT, bool F16, bool LIST>
+__device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const Parts<LIST, RT>& parts,
+                                       Ctrl<D, RT>& c, int tid, bool ok) {
+  constexpr int kU = 8;                          // reads in flight
+  const int np = parts.n;
+  static_assert(sizeof(c.ml) >= kMaxPartsCtas * RT * sizeof(float2), "room for every part");
+  for (int i = tid; i < np * RT; i += 32 * kWarps)
+    c.ml[i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (parts.slot(i / RT) * RT + i % RT) * 2));
+  if (!LIST)
+    for (int i = tid; i < np; i += 32 * kWarps)
+      if (__ldcg(a.part_flag + parts.slot(i))) atomicOr(&c.last, 2);
+  float4 v[kU];
+  auto read = [&](int i, int p0) {
+    const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p0 + u < np && r < it.rows)
+        v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (parts.slot(p0 + u) * RT + r) * D + d4));
+    }
+  };
+  if (tid < RT * (D / 4)) read(tid, 0);
+  compute_sync();
+  for (int i = tid; i < RT * (D / 4); i += 32 * kWarps) {
+    const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
+    if (i != tid) read(i, 0);
+    float mx = -INFINITY, ls = 0.f;
+    for (int p = 0; p < np; ++p) mx = fmaxf(mx, c.ml[p * RT + r].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < np; p0 += kU) {
+      if (p0) read(i, p0);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (p0 + u < np) {
+          const float2 ml = c.ml[(p0 + u) * RT + r];
+          const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+          ls += ml.y * f;
+          add4(acc, v[u], f);
+        }
+      }
+    }
+    if (ok && r < it.rows) store_row4<D, F16, LIST>(a, it, r, d4, acc, mx, ls, c.last & 2);
+  }
+}
 
 }  // namespace
 
@@ -104,15 +184,14 @@ template <int D, int RT, bool F16, bool LIST>
 __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
     const __grid_constant__ PagedArgs a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, RT>;
   constexpr int NT = RT / 8;                    // MMA column tiles of the rows
   constexpr int DM = D / 16;                    // MMA row tiles of the head dim
-  constexpr float kShift = F16 ? 14.f : 0.f;
+  constexpr float kShift = F16 ? 14.f : 0.f;      // (store_row4 takes it back)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl<D, RT>& c = *reinterpret_cast<Ctrl<D, RT>*>(sm + C::kStages * C::kStage);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -151,16 +230,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
       const int ta = (int)(x - it.first), tb = min((int)(xe - it.first), live);
       const int32_t* table = a.g.table + (size_t)it.b * a.g.max_pages;
       const int32_t* list = LIST ? a.kv_idx + (((size_t)it.b * a.g.Hkv + it.h) * a.g.T + it.t) * a.W : nullptr;
-      const int limit = LIST ? it.base + it.t + 1 : it.base + it.ql;     // positions below it are keys
+      // positions below it are keys
+      const int limit = LIST ? (it.t < it.ql ? it.base + it.t + 1 : 0) : it.base + it.ql;
       // Lane i: box (i % npt) of tile t0 + i / npt. The table entries of the batch after this one and
       // the list entries of the one after that are on their way while a batch is issued.
       const int per_load = 32 / npt;
       auto entry = [&](int t0) -> int {          // the box's page number within the sequence, -1: none
         const int tile = t0 + lane / npt;
-        if (tile >= tb) return -1;
+        if (!LIST && tile >= tb) return -1;
         const int e = (tile * kTileKeys + (lane % npt) * rpb) / page;
         if (!LIST) return e * page < limit ? e : -1;
-        return e < cnt ? max(__ldg(list + e), -1) : INT_MIN;
+        if (e >= a.W) return INT_MIN;
+        const int j = __ldg(list + e);           // (within the row of W entries; not behind the count's read)
+        return e < cnt ? max(j, -1) : INT_MIN;
       };
       auto held = [&](int j) -> int {            // its page of the pool
         return j >= 0 && (long long)j * page < limit ? __ldg(table + j) : -1;
@@ -398,88 +480,61 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
           if (lane == 0) tc::mbar_arrive(&c.empty[s]);
         }
 
-        // ---- join the eight states ----
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
-            if (g8 == 0) {
-              c.m[cw][8 * nt + 2 * tig + j] = m[nt][j];
-              c.l[cw][8 * nt + 2 * tig + j] = l[nt][j];
-            }
-          }
-        }
-        compute_sync();
-        float f[NT][2];                          // 2^(m - maximum over the warps)
+        // ---- join the eight states: every warp leaves its own, then a thread adds up four values ----
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float mx = -INFINITY;
+            const int r = 8 * nt + 2 * tig + j;
 #pragma unroll
-            for (int u = 0; u < kWarps; ++u) mx = fmaxf(mx, c.m[u][8 * nt + 2 * tig + j]);
-            f[nt][j] = m[nt][j] == -INFINITY ? 0.f : ex2(m[nt][j] - mx);
-          }
-        // eight turns: in each, every warp adds another eighth of its O (in a fixed order per eighth)
-#pragma unroll 1
-        for (int turn = 0; turn < kWarps; ++turn) {
-          const int e8 = (cw + turn) % kWarps;
-#pragma unroll
-          for (int dm = 0; dm < DM; ++dm)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              if ((DM == 8 ? dm : 2 * dm + hf) != e8) continue;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  float* p = &c.o[8 * nt + 2 * tig + j][16 * dm + 8 * hf + g8];
-                  const float v = o[dm][nt][2 * hf + j] * f[nt][j];
-                  *p = turn == 0 ? v : *p + v;
-                }
+            for (int dm = 0; dm < DM; ++dm) {
+              c.o[cw][r][dump_col(r, 16 * dm + g8)] = o[dm][nt][j];
+              c.o[cw][r][dump_col(r, 16 * dm + g8 + 8)] = o[dm][nt][2 + j];
             }
-          compute_sync();
-        }
-        // ---- result, or partial result ----
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
+            if (g8 == 0) {
+              c.m[cw][r] = m[nt][j];
+              c.l[cw][r] = l[nt][j];
+            }
+          }
+        compute_sync();
         const int tid = threadIdx.x - 32;
         const bool whole = ta == 0 && tend == it.n_tiles;
-        const int fixup = *(volatile int*)&c.flag[seg & 1];
-        const int slot = 2 * blockIdx.x + (ta == 0 ? 1 : 0);
+        const bool fixup = *(volatile int*)&c.flag[seg & 1];
+        const size_t slot = 2 * (size_t)blockIdx.x + (ta == 0 ? 1 : 0);
         for (int i = tid; i < RT * (D / 4); i += 32 * kWarps) {
           const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
           if (r >= it.rows) break;
-          float mx = -INFINITY;
+          float mw[kWarps], mx = -INFINITY, ls = 0.f;
 #pragma unroll
-          for (int u = 0; u < kWarps; ++u) mx = fmaxf(mx, c.m[u][r]);
-          float ls = 0.f;
+          for (int u = 0; u < kWarps; ++u) {
+            mw[u] = c.m[u][r];
+            mx = fmaxf(mx, mw[u]);
+          }
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int u = 0; u < kWarps; ++u) ls += c.m[u][r] == -INFINITY ? 0.f : c.l[u][r] * ex2(c.m[u][r] - mx);
-          float4 v = *reinterpret_cast<const float4*>(&c.o[r][d4]);
+          for (int u = 0; u < kWarps; ++u) {
+            const float f = mw[u] == -INFINITY ? 0.f : ex2(mw[u] - mx);
+            ls += c.l[u][r] * f;
+            add4(v, *reinterpret_cast<const float4*>(&c.o[u][r][dump_col(r, d4)]), f);
+          }
           if (whole) {
-            int head, t;
-            row_of<LIST>(a, it, r, head, t);
-            const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
-            const float inv = ls == 0.f ? 0.f : 1.f / ls;
-            float x4[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-            if (!LIST && fixup) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u) x4[u] += nonfinite_drafts<F16>(a, it, t, d4 + u);
-            }
-            uint2 pk = make_uint2(pack_16<F16>(x4[0], x4[1]), pack_16<F16>(x4[2], x4[3]));
-            if (ok) *reinterpret_cast<uint2*>(a.out + row * D + d4) = pk;
-            if (ok && d4 == 0 && a.lse)
-              a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
+            if (ok) store_row4<D, F16, LIST>(a, it, r, d4, v, mx, ls, fixup);
           } else {
-            *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * RT + r) * D + d4) = v;
-            if (d4 == 0) {
-              a.part_ml[((size_t)slot * RT + r) * 2] = mx;
-              a.part_ml[((size_t)slot * RT + r) * 2 + 1] = ls;
-            }
+            *reinterpret_cast<float4*>(a.part_o + (slot * RT + r) * D + d4) = v;
+            if (d4 == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * RT + r) * 2) = make_float2(mx, ls);
           }
         }
-        if (!whole && tid == 0) a.part_flag[slot] = fixup;
+        if (!whole) {
+          // ---- arrival; the last CTA joins the parts ----
+          if (tid == 0) a.part_flag[slot] = fixup;
+          compute_sync();
+          const Parts<LIST, RT> parts(w, it);
+          if (tid == 0) c.last = arrive_part(a.arrived + parts.c1, parts.n);
+          compute_sync();
+          if (c.last) join_rows<D, RT, F16, LIST>(a, it, parts, c, tid, ok);
+        }
         compute_sync();
         if (tid == 0) c.flag[seg & 1] = 0;       // next used two segments on, behind barriers
       }
@@ -493,114 +548,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
   if (threadIdx.x == 0) {
     for (int t = max(0, tiles_issued - C::kStages); t < tiles_issued; ++t)
       tc::mbar_wait_timed(&c.full[t % C::kStages], (t / C::kStages) & 1);
-    a.cta_status[blockIdx.x] = c.status;
+    wait_prepared();                             // in every CTA: this kernel's end is that one's, too
+    if (c.status) atomicOr(a.dev_status, c.status);
   }
 }
 
 // ---------------------------------------------------------------------------
 
-// Joins the parts of split items: block x does the item that ends in CTA x's share and began in
-// an earlier one, a warp per row. What a row needs of the split is found before the wait for the
-// attention kernel, the weights of the parts sit in the lanes, and the reads of the parts' outputs
-// (16 bytes a lane) do not depend on one another: the kernel is a few memory latencies long.
-constexpr int kJoinWarps = 8;
-
-template <int RT, bool F16, bool LIST>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedArgs a) {
-  constexpr float kShift = F16 ? (RT == 128 ? 7.f : 14.f) : 0.f;
-  const int c = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  Walk<LIST, RT> w;
-  w.init(a);
-  Item it;
-  bool work = false;
-  int c0 = 0;
-  const long long x0 = w.start(c), x1 = w.start(c + 1);
-  if (x0 < x1) {
-    w.locate(a, x0, it);
-    const long long xs = it.first, xe = it.first + it.n_tiles;
-    work = xs < x0 && xe <= x1 && (!LIST || it.t < it.ql);
-    if (work) c0 = w.owner(xs);
+__global__ void __launch_bounds__(256) paged_prepare_kernel(CacheGeom g, int n_cta, int32_t* arrived,
+                                                            int32_t* dev_status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = threadIdx.x; i < n_cta; i += blockDim.x) arrived[i] = 0;
+  bool bad = false;
+  for (int b = threadIdx.x; b < g.slots; b += blockDim.x) {
+    int base, ql;
+    bad |= !query_span(g, b, base, ql);
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c == 0 && blockIdx.y == 0 && warp == 0) {
-    int st = 0;
-    for (int i = lane; i < a.n_cta; i += 32) st |= a.cta_status[i];
-    for (int b = lane; b < a.g.slots; b += 32) {
-      int base, ql;
-      if (!query_span(a.g, b, base, ql)) st |= BSA_DEV_BAD_INDEX;
-    }
-    st = __reduce_or_sync(0xffffffffu, st);
-    if (lane == 0) *a.dev_status = st;
-  }
-  if (!work) return;
-  const int d = a.g.d, np = c - c0 + 1;          // parts: CTA c0's slot 1, the others' slot 0 (none is empty)
-  const int lpr = d / 4;                         // lanes per row of a part: 32 or 16 (two parts at a time)
-  const int dl = (lane % lpr) * 4, half = lane / lpr, step = 32 / lpr;
-  auto row_of_part = [&](int i, int r) { return (2 * (size_t)(c0 + i) + (i == 0 ? 1 : 0)) * RT + r; };
-  for (int r = blockIdx.y * kJoinWarps + warp; r < it.rows; r += kJoinWarps * gridDim.y) {
-    // lane i: maximum and sum of part i, kept when there are no more than 32 parts
-    float2 ml = make_float2(-INFINITY, 0.f);
-    float mx = -INFINITY;
-    int flag = 0;
-    for (int i = lane; i < np; i += 32) {
-      ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row_of_part(i, r) * 2));
-      mx = fmaxf(mx, ml.x);
-      if (!LIST) flag |= __ldcg(a.part_flag + 2 * (c0 + i) + (i == 0 ? 1 : 0));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    flag = __reduce_or_sync(0xffffffffu, flag);
-    float ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < np; i0 += 32) {
-      if (np > 32) {
-        ml = make_float2(-INFINITY, 0.f);
-        if (i0 + lane < np) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row_of_part(i0 + lane, r) * 2));
-      }
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mx);      // lane i: weight of part i0 + i
-      ls += ml.y * f;
-      const int n = min(32, np - i0);
-      constexpr int kU = 8;                                            // reads in flight
-      for (int i = 0; i < n; i += kU * step) {
-        float4 v[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int p = i + u * step + half;
-          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (p < n) v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row_of_part(i0 + p, r) * d + dl));
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int p = i + u * step + half;
-          const float fp = __shfl_sync(0xffffffffu, f, p & 31);
-          if (p < n) {
-            acc[0] = fmaf(v[u].x, fp, acc[0]);
-            acc[1] = fmaf(v[u].y, fp, acc[1]);
-            acc[2] = fmaf(v[u].z, fp, acc[2]);
-            acc[3] = fmaf(v[u].w, fp, acc[3]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-    if (lpr == 16) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) acc[u] += __shfl_xor_sync(0xffffffffu, acc[u], 16);
-    }
-    int head, t;
-    row_of<LIST>(a, it, r, head, t);
-    const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
-    const float inv = ls == 0.f ? 0.f : 1.f / ls;
-    float y[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      y[u] = acc[u] * inv;
-      if (!LIST && flag) y[u] += nonfinite_drafts<F16>(a, it, t, dl + u);
-    }
-    if (half == 0)
-      *reinterpret_cast<uint2*>(a.out + row * d + dl) = make_uint2(pack_16<F16>(y[0], y[1]), pack_16<F16>(y[2], y[3]));
-    if (lane == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
-  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *dev_status = bad ? BSA_DEV_BAD_INDEX : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -614,30 +579,9 @@ int sm_count() {
   return n;
 }
 
-template <int RT, bool F16, bool LIST>
-static cudaError_t join_t(const PagedArgs& a, cudaStream_t st) {
-  // launched behind the attention kernel without waiting for its end; the kernel itself waits
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.n_cta, RT / kJoinWarps);
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<RT, F16, LIST>, a);
-}
-
-template <int RT>
-static cudaError_t join_rt(const PagedArgs& a, bool list, bool f16, cudaStream_t st) {
-  if (f16) return list ? join_t<RT, true, true>(a, st) : join_t<RT, true, false>(a, st);
-  return list ? join_t<RT, false, true>(a, st) : join_t<RT, false, false>(a, st);
-}
-
-cudaError_t launch_paged_join(const PagedArgs& a, int rt, bool list, bool f16, cudaStream_t st) {
-  if (rt == 128) return f16 ? join_t<128, true, false>(a, st) : join_t<128, false, false>(a, st);
-  return rt == 8 ? join_rt<8>(a, list, f16, st) : join_rt<16>(a, list, f16, st);
+cudaError_t launch_paged_prepare(const PagedArgs& a, cudaStream_t st) {
+  paged_prepare_kernel<<<1, 256, 0, st>>>(a.g, a.n_cta, a.arrived, a.dev_status);
+  return cudaGetLastError();
 }
 
 template <int D, int RT, bool F16, bool LIST>
@@ -653,9 +597,11 @@ static cudaError_t attend_t(const bsa_cache_shape& s, const PagedArgs& a, const 
   static_assert(smem <= 227 * 1024, "paged attend shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<a.n_cta, kThreads, smem, st>>>(mk, mv, a);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_paged_join(a, RT, LIST, F16, st);
+  e = launch_paged_prepare(a, st);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  const cudaLaunchConfig_t cfg = beside(at, a.n_cta, kThreads, smem, st);
+  return cudaLaunchKernelEx(&cfg, kern, mk, mv, a);
 }
 
 template <int D, int RT>

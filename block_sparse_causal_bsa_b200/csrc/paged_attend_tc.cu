@@ -58,6 +58,7 @@ struct __align__(16) Ctrl {
   int abort_flag;
   int32_t status;
   int flag[2];                                  // by segment parity: non-finite drafts taken out
+  int last;                                     // this CTA joins the item's parts
 };
 
 template <int D>
@@ -93,6 +94,75 @@ __device__ __forceinline__ uint64_t draft_window(const PagedArgs& a, int b, int 
   return x;
 }
 
+// Parts lie transposed, [D / 4][RT] of four floats: a warp's rows are then neighbours both when a
+// part is written (a thread per row) and when parts are joined.
+__device__ __forceinline__ float4* part4(const PagedArgs& a, size_t slot, int D, int d4, int r) {
+  return reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + d4) * RT + r;
+}
+
+// Joins the parts of an item, the four softmax warps: 128 / R threads per row, R the rows rounded up
+// to whole warps; eight reads of 16 bytes in flight per thread.
+template <int D, bool F16>
+__device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const Parts<false, RT>& parts, int tid,
+                                       bool ok) {
+  constexpr float kShift = F16 ? 7.f : 0.f;
+  constexpr int kU = 8;
+  const int np = parts.n, R = (it.rows + 31) / 32 * 32;
+  const int groups = 128 / R, r = tid % R, dg = tid / R;       // (R = 96: one group, 32 threads idle)
+  if (dg >= groups || r >= it.rows) return;
+  float mx = -INFINITY, ls = 0.f;
+  int flag = 0;
+#pragma unroll 8
+  for (int i = 0; i < np; ++i) {
+    mx = fmaxf(mx, __ldcg(a.part_ml + (parts.slot(i) * RT + r) * 2));
+    flag |= __ldcg(a.part_flag + parts.slot(i));
+  }
+  int head, t;
+  row_of<false>(a, it, r, head, t);
+  const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
+  for (int d0 = dg; d0 < D / 4; d0 += groups * kU) {
+    float4 acc[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    ls = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < np; ++i) {
+      const size_t slot = parts.slot(i);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (slot * RT + r) * 2));
+      float4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (d0 + u * groups < D / 4) v[u] = __ldcg(part4(a, slot, D, d0 + u * groups, r));
+      }
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+      ls += ml.y * f;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        acc[u].x = fmaf(v[u].x, f, acc[u].x);
+        acc[u].y = fmaf(v[u].y, f, acc[u].y);
+        acc[u].z = fmaf(v[u].z, f, acc[u].z);
+        acc[u].w = fmaf(v[u].w, f, acc[u].w);
+      }
+    }
+    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int d4 = d0 + u * groups;
+      if (d4 >= D / 4) break;
+      float y[4] = {acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv};
+      if (flag) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += nonfinite_drafts<F16>(a, it, t, 4 * d4 + e);
+      }
+      if (ok)
+        *reinterpret_cast<uint2*>(a.out + row * D + 4 * d4) =
+            make_uint2(pack_16<F16>(y[0], y[1]), pack_16<F16>(y[2], y[3]));
+    }
+  }
+  if (ok && dg == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
+}
+
 }  // namespace
 
 template <int D, bool F16>
@@ -107,7 +177,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
   Ctrl& c = *reinterpret_cast<Ctrl*>(sm + C::kCtrl);
   const uint32_t sQ = tc::smem_u32(sm + C::kQ), sK = tc::smem_u32(sm + C::kK), sV = tc::smem_u32(sm + C::kV);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  launch_dependents();
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&c.q_full, 4);
@@ -439,9 +508,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
                              pack_16<F16>(y[6], y[7]));
             }
           } else if (r < it.rows) {
-            uint4* po = reinterpret_cast<uint4*>(a.part_o + (slot * RT + r) * D + cc * 32);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) po[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(part4(a, slot, D, cc * 8 + i, r)) =
+                  make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
         if (r < it.rows) {
@@ -449,14 +519,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
             if (a.lse)
               a.lse[grow] = l == 0.f ? -INFINITY : (m_used - kShift + log2f(l)) * 0.69314718055994531f;
           } else {
-            a.part_ml[(slot * RT + r) * 2] = m_used;
-            a.part_ml[(slot * RT + r) * 2 + 1] = l;
+            *reinterpret_cast<float2*>(a.part_ml + (slot * RT + r) * 2) = make_float2(m_used, l);
           }
         }
         __syncwarp();
         tc::tc_fence_before();
       }
-      if (!whole && tid == 0) a.part_flag[slot] = fixup;
+      if (!whole) {
+        // ---- arrival; the last CTA joins the parts ----
+        if (tid == 0) a.part_flag[slot] = fixup;
+        softmax_sync();
+        const Parts<false, RT> parts(w, it);
+        if (tid == 0) c.last = arrive_part(a.arrived + parts.c1, parts.n);
+        softmax_sync();
+        if (c.last) join_rows<D, F16>(a, it, parts, tid, ok);
+      }
       softmax_sync();
       if (tid == 0) c.flag[seg & 1] = 0;                 // next used two segments on, behind barriers
       x = xe;
@@ -470,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
   if (threadIdx.x == 0) {
     for (int j = max(0, k_issued - NS); j < k_issued; ++j) tc::mbar_wait_timed(&c.k_full[j % NS], (j / NS) & 1);
     for (int j = max(0, v_issued - NS); j < v_issued; ++j) tc::mbar_wait_timed(&c.v_full[j % NS], (j / NS) & 1);
-    a.cta_status[blockIdx.x] = c.status;
+    wait_prepared();                             // in every CTA: this kernel's end is that one's, too
+    if (c.status) atomicOr(a.dev_status, c.status);
   }
   if (warp == 1) {
     if (lane == 0 && mma_issued) {
@@ -496,9 +574,11 @@ static cudaError_t attend_tc_t(const bsa_cache_shape& s, const PagedArgs& a, con
   static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<a.n_cta, kThreads, smem, st>>>(mk, mv, a);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_paged_join(a, RT, false, F16, st);
+  e = launch_paged_prepare(a, st);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  const cudaLaunchConfig_t cfg = beside(at, a.n_cta, kThreads, smem, st);
+  return cudaLaunchKernelEx(&cfg, kern, mk, mv, a);
 }
 
 cudaError_t launch_paged_attend_tc(const bsa_cache_shape& s, const PagedArgs& a, const void* k, const void* v,

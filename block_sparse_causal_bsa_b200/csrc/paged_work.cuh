@@ -9,8 +9,12 @@
 // contiguous share of them, so ragged lengths balance without the host knowing them. A share may
 // begin or end inside an item: such segments leave a partial result (running maximum, sum,
 // unnormalised output) in one of the CTA's two slots of the workspace, 0 for a segment that starts
-// inside its item, 1 for one that starts with it, and a second kernel joins them. The split depends on
-// lengths alone, so results repeat bit for bit.
+// inside its item, 1 for one that starts with it. The CTA that arrives last at an item's counter joins its
+// parts, in their order along the keys whichever CTA that is: the split depends on lengths alone, and
+// results repeat bit for bit. (A second kernel for the joins took 28 us behind 354 us of attention for
+// wide trees and 7 to 12 us behind small calls, most of it spent on finding the split again.)
+// A small kernel zeroes the counters first. The attention kernel starts beside it (programmatic
+// serialization) and waits for it only before its first arrival.
 #pragma once
 
 #include "common.cuh"
@@ -36,7 +40,7 @@ struct PagedArgs {
   float* part_o;                    // [2 * n_cta][RT][d]
   float* part_ml;                   // [2 * n_cta][RT][2]
   int32_t* part_flag;               // [2 * n_cta]
-  int32_t* cta_status;              // [n_cta]
+  int32_t* arrived;                 // [n_cta]: parts of the item that ends in the CTA's share
   int32_t* dev_status;
   int n_cta;
 };
@@ -53,22 +57,38 @@ struct Item {
   long long first;                  // its first tile in the whole order
 };
 
+// How far a share may shrink: below this many tiles per CTA the arrival and the join cost more time
+// than the shorter share saves.
+template <int RT>
+constexpr int kMinTiles = RT == 128 ? 2 : 4;
+
 template <bool LIST, int RT>
 struct Walk {
   long long total;                  // tiles of all items
   long long per;                    // tiles per CTA (the last ones may have fewer, or none)
+  // lane b (whole cache): slot b's tiles and tokens
+  long long tiles;
+  int base, ql;
 
   __device__ static int slot_items(const PagedArgs& a, int ql) {
     return a.g.Hkv * ceil_div_i(a.G * ql, RT);
   }
-  // tiles of all items of slot b
-  __device__ static long long slot_tiles(const PagedArgs& a, int b) {
-    int base, ql;
-    query_span(a.g, b, base, ql);
+  __device__ static long long slot_tiles(const PagedArgs& a, int base, int ql) {
     return ql ? (long long)slot_items(a, ql) * ceil_div_i(base + ql, kTileKeys) : 0;
   }
   __device__ static int list_tiles(const PagedArgs& a) {
     return (int)(((long long)a.W * a.g.page + kTileKeys - 1) / kTileKeys);
+  }
+  // (64-bit divisions are slow)
+  __device__ static long long divide(long long x, long long y) {
+    return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+  }
+  // slot b0 + lane
+  __device__ void load(const PagedArgs& a, int b0) {
+    const int b = b0 + threadIdx.x % 32;
+    base = ql = 0;
+    if (b < a.g.slots) query_span(a.g, b, base, ql);
+    tiles = slot_tiles(a, base, ql);
   }
 
   // Whole warp.
@@ -76,21 +96,20 @@ struct Walk {
     if (LIST) {
       total = (long long)a.g.slots * a.g.Hkv * a.g.T * list_tiles(a);
     } else {
-      const int lane = threadIdx.x % 32;
       long long s = 0;
-      for (int b = lane; b < a.g.slots; b += 32) s += slot_tiles(a, b);
+      for (int b0 = (a.g.slots - 1) / 32 * 32; b0 >= 0; b0 -= 32) {    // (the first slots stay loaded)
+        load(a, b0);
+        s += tiles;
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       total = s;
     }
-    const long long n = total + a.n_cta - 1;         // (64-bit divisions are slow)
-    per = n >> 32 ? n / a.n_cta : (long long)((uint32_t)n / (uint32_t)a.n_cta);
+    per = max(divide(total + a.n_cta - 1, a.n_cta), (long long)kMinTiles<RT>);
   }
   __device__ long long start(int c) const { return min(c * per, total); }
   // the CTA whose share holds tile x
-  __device__ int owner(long long x) const {
-    return x >> 32 || per >> 32 ? (int)(x / per) : (int)((uint32_t)x / (uint32_t)per);
-  }
+  __device__ int owner(long long x) const { return (int)divide(x, per); }
 
   __device__ void set_list_item(const PagedArgs& a, long long item, Item& it) const {
     it.n_tiles = list_tiles(a);
@@ -103,31 +122,28 @@ struct Walk {
     it.row0 = 0;
     it.rows = a.G;
   }
-  __device__ void set_slot_item(const PagedArgs& a, int b, long long slot_first, int item, Item& it) const {
-    query_span(a.g, b, it.base, it.ql);
-    it.b = b;
+  // it.b, it.base and it.ql are set
+  __device__ void set_slot_item(const PagedArgs& a, long long slot_first, int item, Item& it) const {
     it.n_tiles = ceil_div_i(it.base + it.ql, kTileKeys);
     it.first = slot_first + (long long)item * it.n_tiles;
     const int M = a.G * it.ql, mts = ceil_div_i(M, RT);
-    it.h = item / mts;
-    it.row0 = (item % mts) * RT;
+    it.h = mts == 1 ? item : item / mts;
+    it.row0 = (item - it.h * mts) * RT;
     it.rows = min(RT, M - it.row0);
     it.t = 0;
   }
 
   // The item of tile x (0 <= x < total). Whole warp.
-  __device__ void locate(const PagedArgs& a, long long x, Item& it) const {
+  __device__ void locate(const PagedArgs& a, long long x, Item& it) {
     if (LIST) {
-      const int n = list_tiles(a);
-      set_list_item(a, x >> 32 ? x / n : (long long)((uint32_t)x / (uint32_t)n), it);
+      set_list_item(a, divide(x, list_tiles(a)), it);
       return;
     }
     const int lane = threadIdx.x % 32;
     long long before = 0;
     for (int b0 = 0; b0 < a.g.slots; b0 += 32) {
-      const int b = b0 + lane;
-      const long long w = b < a.g.slots ? slot_tiles(a, b) : 0;
-      long long p = w;                              // inclusive prefix
+      if (b0) load(a, b0);
+      long long p = tiles;                          // inclusive prefix
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, p, o);
@@ -136,12 +152,11 @@ struct Walk {
       const unsigned m = __ballot_sync(0xffffffffu, before + p > x);
       if (m) {
         const int l = __ffs(m) - 1;
-        const long long first = before + __shfl_sync(0xffffffffu, p - w, l);
-        int base, ql;
-        query_span(a.g, b0 + l, base, ql);
-        const long long off = x - first;
-        const int nt = ceil_div_i(base + ql, kTileKeys);
-        set_slot_item(a, b0 + l, first, off >> 32 ? (int)(off / nt) : (int)((uint32_t)off / (uint32_t)nt), it);
+        const long long first = before + __shfl_sync(0xffffffffu, p - tiles, l);
+        it.b = b0 + l;
+        it.base = __shfl_sync(0xffffffffu, base, l);
+        it.ql = __shfl_sync(0xffffffffu, ql, l);
+        set_slot_item(a, first, (int)divide(x - first, ceil_div_i(it.base + it.ql, kTileKeys)), it);
         return;
       }
       before += __shfl_sync(0xffffffffu, p, 31);
@@ -157,12 +172,14 @@ struct Walk {
     const int mts = ceil_div_i(a.G * it.ql, RT);
     const int item = it.h * mts + it.row0 / RT + 1;
     if (item < a.g.Hkv * mts) {
-      set_slot_item(a, it.b, it.first - (long long)(item - 1) * it.n_tiles, item, it);
+      set_slot_item(a, it.first - (long long)(item - 1) * it.n_tiles, item, it);
       return;
     }
-    int b = it.b + 1;
-    while (slot_tiles(a, b) == 0) ++b;
-    set_slot_item(a, b, x, 0, it);
+    do {
+      ++it.b;
+      query_span(a.g, it.b, it.base, it.ql);
+    } while (it.ql == 0);
+    set_slot_item(a, x, 0, it);
   }
 };
 
@@ -199,10 +216,6 @@ __device__ __forceinline__ bool sees_draft(const PagedArgs& a, int b, int t, int
   if (!a.mask) return j <= t;
   return (a.mask[((size_t)b * a.g.T + t) * a.words + (j >> 6)] >> (j & 63)) & 1ull;
 }
-
-// The kernel launched behind this one (with programmatic serialization) may start its blocks as
-// room appears; it waits for the end of this one itself before it reads results.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <bool F16>
 __device__ __forceinline__ float cvt_f32(uint16_t x) {
@@ -258,9 +271,46 @@ __device__ __noinline__ float nonfinite_drafts(const PagedArgs& a, const Item& i
   return s;
 }
 
-// Joins the partial results of the items that are split over CTAs (a warp per row), and gathers
-// the status words. The scale of fp16 weights cancels, but for the lse: shift is its exponent.
-cudaError_t launch_paged_join(const PagedArgs& a, int rt, bool list, bool f16, cudaStream_t st);
+// What waits for the preparing kernel (counters and *dev_status are set when it returns).
+__device__ __forceinline__ void wait_prepared() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The parts of a split item: CTAs c0 .. c1, and the slot of the part of CTA c0 + i.
+template <bool LIST, int RT>
+struct Parts {
+  int c0, n, c1;
+  __device__ Parts(const Walk<LIST, RT>& w, const Item& it) {
+    c0 = w.owner(it.first);
+    c1 = w.owner(it.first + it.n_tiles - 1);
+    n = c1 - c0 + 1;
+  }
+  __device__ size_t slot(int i) const { return 2 * (size_t)(c0 + i) + (i == 0 ? 1 : 0); }
+};
+
+// One thread, behind a barrier that the CTA's writes of its part precede: counts the part in; true
+// for the last one, whose CTA joins them (behind another barrier).
+__device__ __forceinline__ bool arrive_part(int32_t* counter, int n) {
+  wait_prepared();
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old == n - 1;
+}
+
+// Zeroes the counters and sets *dev_status to what the lengths say.
+cudaError_t launch_paged_prepare(const PagedArgs& a, cudaStream_t st);
+
+// Launch attributes of a kernel that may start beside the one before it.
+inline cudaLaunchConfig_t beside(cudaLaunchAttribute* at, unsigned grid, unsigned block, size_t smem, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
 
 // Attention on warp-level MMAs (row tiles of 8 or 16).
 cudaError_t launch_paged_attend_mma(const bsa_cache_shape& s, PagedArgs a, const void* k, const void* v,
@@ -269,6 +319,9 @@ cudaError_t launch_paged_attend_mma(const bsa_cache_shape& s, PagedArgs a, const
 // The same on tcgen05 (row tiles of 128, whole cache only; a.n_cta: two per SM).
 cudaError_t launch_paged_attend_tc(const bsa_cache_shape& s, const PagedArgs& a, const void* k, const void* v,
                                    cudaStream_t st);
+
+// CTAs at most of the kernel on warp-level MMAs (its join keeps every part's maxima in shared memory).
+constexpr int kMaxPartsCtas = 256;
 
 // Query rows per KV head up to which a call runs on warp-level MMAs.
 constexpr int kMaxMmaRows = 16;
