@@ -93,7 +93,9 @@ struct AttendWs {
   float* part_ml;
   int32_t* part_flag;
   int32_t* arrived;
-  int n_cta;
+  float* half_o;
+  float* half_ml;
+  int n_cta, n_arrived;
   bool tc;
   size_t bytes;
 };
@@ -102,16 +104,21 @@ AttendWs attend_ws(const bsa_cache_shape& s, int Hq, int T, bool list, void* bas
   AttendWs w{};
   const int rows = (Hq / s.Hkv) * (list ? 1 : T);
   const bool tc = rows > bsa::kMaxMmaRows;
-  const int rt = tc ? 128 : (rows <= 8 ? 8 : 16);
-  w.n_cta = tc ? 2 * bsa::sm_count() : std::min(bsa::sm_count(), bsa::kMaxPartsCtas);
+  const int rt = tc ? 256 : (rows <= 8 ? 8 : 16);
+  w.n_cta = std::min(bsa::sm_count(), bsa::kMaxPartsCtas);
+  w.n_arrived = (tc ? 2 : 1) * w.n_cta;
   w.tc = tc;
   const size_t slots = 2 * (size_t)w.n_cta;
   char* p = (char*)base;
   size_t off = 0;
   w.part_o = (float*)(p + off); off += align256(slots * rt * s.d * 4);
   w.part_ml = (float*)(p + off); off += align256(slots * rt * 2 * 4);
-  w.part_flag = (int32_t*)(p + off); off += align256(slots * 4);
-  w.arrived = (int32_t*)(p + off); off += align256((size_t)w.n_cta * 4);
+  w.part_flag = (int32_t*)(p + off); off += align256(2 * slots * 4);
+  w.arrived = (int32_t*)(p + off); off += align256((size_t)w.n_arrived * 4);
+  if (tc) {
+    w.half_o = (float*)(p + off); off += align256(slots * 128 * s.d * 4);
+    w.half_ml = (float*)(p + off); off += align256(slots * 128 * 2 * 4);
+  }
   w.bytes = off;
   return w;
 }
@@ -165,6 +172,9 @@ bsa_status attend(const bsa_cache_shape* s, int slots, int max_pages, int Hq, in
   a.part_ml = w.part_ml;
   a.part_flag = w.part_flag;
   a.arrived = w.arrived;
+  a.n_arrived = w.n_arrived;
+  a.half_o = w.half_o;
+  a.half_ml = w.half_ml;
   a.dev_status = dev_status;
   a.n_cta = w.n_cta;
   cudaStream_t cs = (cudaStream_t)stream;

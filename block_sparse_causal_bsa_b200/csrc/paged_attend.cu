@@ -555,10 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
 
 // ---------------------------------------------------------------------------
 
-__global__ void __launch_bounds__(256) paged_prepare_kernel(CacheGeom g, int n_cta, int32_t* arrived,
+__global__ void __launch_bounds__(256) paged_prepare_kernel(CacheGeom g, int n, int32_t* arrived,
                                                             int32_t* dev_status) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int i = threadIdx.x; i < n_cta; i += blockDim.x) arrived[i] = 0;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) arrived[i] = 0;
   bool bad = false;
   for (int b = threadIdx.x; b < g.slots; b += blockDim.x) {
     int base, ql;
@@ -580,7 +580,7 @@ int sm_count() {
 }
 
 cudaError_t launch_paged_prepare(const PagedArgs& a, cudaStream_t st) {
-  paged_prepare_kernel<<<1, 256, 0, st>>>(a.g, a.n_cta, a.arrived, a.dev_status);
+  paged_prepare_kernel<<<1, 256, 0, st>>>(a.g, a.n_arrived, a.arrived, a.dev_status);
   return cudaGetLastError();
 }
 

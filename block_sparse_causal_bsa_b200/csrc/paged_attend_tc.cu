@@ -1,22 +1,26 @@
-// Attention over a paged cache on tcgen05: trees and chains of drafted tokens, up to 128 query
+// Attention over a paged cache on tcgen05: trees and chains of drafted tokens, up to 256 query
 // rows (heads of a KV group x tokens) per item.
 //
 //   O = sum softmax(scale q.k) v over the positions a token sees
 //
-// 128 rows against a key cost 4 * 128 * d flops for the 4 d bytes of its K and V: with full tiles the
-// tensor cores and the exponentials bound the kernel, with few rows the HBM reads of the cache.
-// Two CTAs per SM (192 threads, 256 TMEM columns, ~100 KB of shared memory each), each
-// walking its share of all key tiles (paged_work.cuh), so that one's softmax overlaps the other's
-// products and loads:
-//   warp 0     producer: page numbers in its lanes' registers, then per tile one TMA box per page and
-//              64-column half, K and V in separate stages
-//   warp 1     one thread issues S_n = Q K_n^T into one of two TMEM buffers, S_{n+1} before the value product of
-//              tile n, and O += P_n V_n with P read from TMEM
-//   warps 2-5  a thread per row: Q of the item into shared memory (128-byte swizzle, as TMA would write
-//              it), then per tile S from TMEM, the mask where the tile needs one, the online
-//              softmax (O rescaled in TMEM only when the maximum grew by more than 2^8), P in 16
-//              bits over the S just read; O / l or the partial result at the end of a segment. Warps whose
-//              rows are all past the item's skip the arithmetic.
+// A key costs 4 d flops per row for the 4 d bytes of its K and V: from some 250 rows on the products
+// bound the kernel, below that the HBM reads of the cache, and between them the exponentials (one
+// per row and key, 16 a clock and SM) are never far behind. So every K and V tile is read once for up to
+// 256 rows, and two independent chains of products and softmax share it. One CTA per SM, 384
+// threads, all 512 columns of TMEM, walking its share of all key tiles (paged_work.cuh):
+//   warp 0      producer: page numbers in its lanes' registers, then per tile one TMA box per page and
+//               64-column half, K and V in separate stages
+//   warps 1, 2  one thread each issues the products of group 0 and of group 1: S_j = Q K_j^T into one of
+//               two TMEM buffers, S of the group's next tile before the value product of this one,
+//               and O += P_j V_j with P read from TMEM
+//   warps 4-7, 8-11  softmax of groups 0 and 1, a thread per row: Q of the item into shared memory
+//               (128-byte swizzle, as TMA would write it), then per tile S from TMEM, the mask where
+//               the tile needs one, the online softmax (O rescaled in TMEM only when the maximum grew
+//               by more than 2^8), P in 16 bits over the S just read; O / l or the partial result at the end
+//               of a segment. Warps whose rows are all past the item's skip the arithmetic.
+// Items of more than 128 rows: group 1 takes rows 128 and up, both groups every tile. Items of up to
+// 128 rows: both groups take the same rows and every other tile, and group 0 adds up the two states at
+// the end of a segment (group 1 leaves its own in the workspace, two areas in turn).
 // P is rounded to 16 bits, a relative 2^-9 (bf16) or 2^-12 (fp16) per weight, within the rounding of the
 // output; sums and maxima are fp32. For fp16, weights carry a factor 2^7: with the maximum up to 2^8
 // stale they stay below 2^15, and weights down to 2^-31 of the largest still count.
@@ -31,34 +35,40 @@ namespace bsa {
 
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int RT = 128;
+constexpr int kThreads = 384;
+constexpr int RT = 256;
+constexpr int GR = 128;                         // rows of a group
 constexpr int kMaskRing = 16;
-constexpr uint32_t kTmemCols = 256;
-constexpr uint32_t kColO = 0;                   // O accumulator
-constexpr uint32_t kColS = 128;                 // S buffers at 128 and 192
+constexpr uint32_t kTmemCols = 512;             // group g: O at 256 g, S buffers at 256 g + 128 and + 192
+constexpr uint32_t kColS = 128;
 
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
-  static constexpr uint32_t kQHalf = RT * 128;
+  static constexpr uint32_t kQHalf = GR * 128;
+  static constexpr uint32_t kQTile = kHalves * kQHalf;
   static constexpr uint32_t kHalf = kTileKeys * 128;
   static constexpr uint32_t kTile = kHalves * kHalf;
-  static constexpr int NS = D == 128 ? 2 : 4;
-  static constexpr size_t kQ = 0, kK = kHalves * kQHalf, kV = kK + NS * kTile, kCtrl = kV + NS * kTile;
+  static constexpr int NS = D == 128 ? 5 : 8;
+  static constexpr size_t kQ = 0, kK = 2 * kQTile, kV = kK + NS * kTile, kCtrl = kV + NS * kTile;
 };
+constexpr int kMaxStages = 8;
+static_assert(kMaskRing > kMaxStages, "the producer is at most a ring ahead of the softmax");
 
-struct __align__(16) Ctrl {
+struct Group {                                  // barriers of one group
   uint64_t q_full;
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2];
   uint64_t p_full, o_ready, done;
+};
+struct __align__(16) Ctrl {
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
+  Group g[2];
   unsigned long long vmask[kMaskRing];          // by tile: rows that are keys
   uint32_t tmem;
   int abort_flag;
   int32_t status;
-  int flag[2];                                  // by segment parity: non-finite drafts taken out
-  int last;                                     // this CTA joins the item's parts
+  int flag[2][2];                               // [group][segment parity]: non-finite drafts taken out
+  int last[2];                                  // [group]: this CTA joins the item's parts
 };
 
 template <int D>
@@ -76,7 +86,9 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
       "add.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
       : "+f"(a0), "+f"(a1) : "f"(b0), "f"(b1));
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// the four softmax warps of a group; both groups
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
+__device__ __forceinline__ void both_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 // Keys of the tile that starts dj positions after the slot's first token (dj may be negative) that
 // token t sees: bit i for key i.
@@ -99,23 +111,31 @@ __device__ __forceinline__ uint64_t draft_window(const PagedArgs& a, int b, int 
 __device__ __forceinline__ float4* part4(const PagedArgs& a, size_t slot, int D, int d4, int r) {
   return reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + d4) * RT + r;
 }
+// Group 1's state of a segment whose tiles the groups share: area `par` of the CTA.
+__device__ __forceinline__ float4* half4(const PagedArgs& a, int par, int D, int d4, int r) {
+  return reinterpret_cast<float4*>(a.half_o) + ((2 * (size_t)blockIdx.x + par) * (D / 4) + d4) * GR + r;
+}
+__device__ __forceinline__ float2* half_ml(const PagedArgs& a, int par, int r) {
+  return reinterpret_cast<float2*>(a.half_ml) + (2 * (size_t)blockIdx.x + par) * GR + r;
+}
 
-// Joins the parts of an item, the four softmax warps: 128 / R threads per row, R the rows rounded up
-// to whole warps; eight reads of 16 bytes in flight per thread.
+// Joins the parts of a group's rows [r0, r0 + rows) of an item, its four softmax warps: 128 / R threads per
+// row, R the rows rounded up to whole warps; eight reads of 16 bytes in flight per thread.
 template <int D, bool F16>
-__device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const Parts<false, RT>& parts, int tid,
-                                       bool ok) {
+__device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const Parts<false, RT>& parts, int r0,
+                                       int rows, int tid, bool ok) {
   constexpr float kShift = F16 ? 7.f : 0.f;
   constexpr int kU = 8;
-  const int np = parts.n, R = (it.rows + 31) / 32 * 32;
-  const int groups = 128 / R, r = tid % R, dg = tid / R;       // (R = 96: one group, 32 threads idle)
-  if (dg >= groups || r >= it.rows) return;
+  const int np = parts.n, R = (rows + 31) / 32 * 32;
+  const int groups = 128 / R, dg = tid / R;                    // (R = 96: one group, 32 threads idle)
+  if (dg >= groups || tid % R >= rows) return;
+  const int r = r0 + tid % R;
   float mx = -INFINITY, ls = 0.f;
   int flag = 0;
 #pragma unroll 8
   for (int i = 0; i < np; ++i) {
     mx = fmaxf(mx, __ldcg(a.part_ml + (parts.slot(i) * RT + r) * 2));
-    flag |= __ldcg(a.part_flag + parts.slot(i));
+    flag |= __ldcg(a.part_flag + 2 * parts.slot(i) + (r0 ? 1 : 0));
   }
   int head, t;
   row_of<false>(a, it, r, head, t);
@@ -166,7 +186,7 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
 }  // namespace
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
+__global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
     const __grid_constant__ PagedArgs a) {
   using C = Cfg<D>;
@@ -179,26 +199,28 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    tc::mbar_init(&c.q_full, 4);
     for (int s = 0; s < NS; ++s) {
       tc::mbar_init(&c.k_full[s], 1);
-      tc::mbar_init(&c.k_empty[s], 1);
       tc::mbar_init(&c.v_full[s], 1);
-      tc::mbar_init(&c.v_empty[s], 1);
+      tc::mbar_init(&c.k_empty[s], 2);          // both issuers
+      tc::mbar_init(&c.v_empty[s], 2);
     }
-    // the issuing thread arrives itself, too: what it saw (the tile's mask) is then visible to
-    // the softmax warps
-    tc::mbar_init(&c.s_full[0], 2);
-    tc::mbar_init(&c.s_full[1], 2);
-    tc::mbar_init(&c.p_full, 4);
-    tc::mbar_init(&c.o_ready, 1);
-    tc::mbar_init(&c.done, 1);
+    for (int g = 0; g < 2; ++g) {
+      tc::mbar_init(&c.g[g].q_full, 4);
+      // the issuing thread arrives itself, too: what it saw (the tile's mask) is then visible to
+      // the softmax warps
+      tc::mbar_init(&c.g[g].s_full[0], 2);
+      tc::mbar_init(&c.g[g].s_full[1], 2);
+      tc::mbar_init(&c.g[g].p_full, 4);
+      tc::mbar_init(&c.g[g].o_ready, 1);
+      tc::mbar_init(&c.g[g].done, 1);
+      c.flag[g][0] = c.flag[g][1] = 0;
+    }
     c.abort_flag = 0;
     c.status = 0;
-    c.flag[0] = c.flag[1] = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == 3) {
     tc::tmem_alloc(&c.tmem, kTmemCols);
     tc::tmem_relinquish();
   }
@@ -287,59 +309,79 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
       x = xe;
       if (x < x1) w.next(a, it);
     }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
+  } else if (warp <= 2) {
+    // ---------------- MMA issuers ----------------
     // (the walk is the whole warp's; one lane waits and issues)
     constexpr uint32_t idS = F16 ? tc::idesc_f16_f32(128, 64, false, false) : tc::idesc_bf16_f32(128, 64, false, false);
     constexpr uint32_t idPV = F16 ? tc::idesc_f16_f32(128, D, false, true) : tc::idesc_bf16_f32(128, D, false, true);
-    int n = 0, seg = 0;
+    const int g = warp - 1;
+    Group& b = c.g[g];
+    const uint32_t sQg = sQ + g * C::kQTile, tg = tmem + g * 256;
+    int n = 0, seg = 0, js = 0, jv = 0;          // tiles of the CTA; products of this group issued
     bool ok = true;
     for (long long x = x0; x < x1; ++seg) {
       const long long xe = min(x1, it.first + it.n_tiles);
       const int L = (int)(xe - x);
       if (lane == 0 && ok) {
-        auto issue_s = [&](int j) {
-          const uint32_t kb = sK + (j % NS) * C::kTile;
-          const uint32_t d = tmem + kColS + (j % 2) * 64;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t qoff = (kk >> 2) * C::kQHalf + (kk & 3) * 32;
-            const uint32_t koff = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-            tc::umma_bf16(d, tc::sdesc_sw128(sQ + qoff, 16, 1024), tc::sdesc_sw128(kb + koff, 16, 1024), idS, kk > 0);
-          }
-          tc::mbar_arrive(&c.s_full[j % 2]);
-          tc::umma_commit(&c.s_full[j % 2]);
-          tc::umma_commit(&c.k_empty[j % NS]);
-        };
-        ok = tc::mbar_wait(&c.q_full, seg & 1, abort_flag, status) &&
-             tc::mbar_wait(&c.k_full[n % NS], (n / NS) & 1, abort_flag, status);
-        if (ok) {
-          tc::tc_fence_after();
-          issue_s(n);
-          mma_issued = true;
-        }
-        for (int i = 0; ok && i < L; ++i) {
-          const int j = n + i, jn = j + 1;
-          if (i + 1 < L) {
-            // S(jn) overwrites the buffer whose P the value product of tile jn - 2 reads
-            ok = tc::mbar_wait(&c.k_full[jn % NS], (jn / NS) & 1, abort_flag, status) &&
-                 (jn < 2 || tc::mbar_wait(&c.o_ready, (jn - 2) & 1, abort_flag, status));
+        const bool share = it.rows <= GR;        // the groups take the tiles in turn
+        int si = 0;                              // next tile of the segment to be looked at for S
+        const int js0 = js;
+        // S of the group's next tile; the tiles of the other group on the way are released
+        auto next_s = [&]() {
+          for (bool mine = false; ok && !mine && si < L; ++si) {
+            const int s = (n + si) % NS;
+            ok = tc::mbar_wait(&c.k_full[s], ((n + si) / NS) & 1, abort_flag, status);
+            if (!ok) break;
+            mine = !share || ((n + si) & 1) == g;
+            if (!mine) {
+              tc::mbar_arrive(&c.k_empty[s]);
+              continue;
+            }
+            // S overwrites the buffer whose P the value product of two tiles ago read. (For the first of
+            // a segment every product has landed, as Q's arrival says; the parity of two ago would
+            // wait for the next one.)
+            if (js >= 2 && js > js0) ok = tc::mbar_wait(&b.o_ready, js & 1, abort_flag, status);
             if (!ok) break;
             tc::tc_fence_after();
-            issue_s(jn);
+            const uint32_t kb = sK + s * C::kTile, d = tg + kColS + (js % 2) * 64;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t qoff = (kk >> 2) * C::kQHalf + (kk & 3) * 32;
+              const uint32_t koff = (kk >> 2) * C::kHalf + (kk & 3) * 32;
+              tc::umma_bf16(d, tc::sdesc_sw128(sQg + qoff, 16, 1024), tc::sdesc_sw128(kb + koff, 16, 1024), idS, kk > 0);
+            }
+            tc::mbar_arrive(&b.s_full[js % 2]);
+            tc::umma_commit(&b.s_full[js % 2]);
+            tc::umma_commit(&c.k_empty[s]);
+            mma_issued = true;
+            ++js;
           }
-          ok = tc::mbar_wait(&c.v_full[j % NS], (j / NS) & 1, abort_flag, status) &&
-               tc::mbar_wait(&c.p_full, j & 1, abort_flag, status);
+        };
+        ok = tc::mbar_wait(&b.q_full, seg & 1, abort_flag, status);
+        if (ok) next_s();
+        bool first = true;
+        for (int i = 0; ok && i < L; ++i) {
+          const int s = (n + i) % NS;
+          if (share && ((n + i) & 1) != g) {
+            ok = tc::mbar_wait(&c.v_full[s], ((n + i) / NS) & 1, abort_flag, status);
+            if (ok) tc::mbar_arrive(&c.v_empty[s]);
+            continue;
+          }
+          next_s();
+          if (!ok) break;
+          ok = tc::mbar_wait(&c.v_full[s], ((n + i) / NS) & 1, abort_flag, status) &&
+               tc::mbar_wait(&b.p_full, jv & 1, abort_flag, status);
           if (!ok) break;
           tc::tc_fence_after();
-          const uint32_t vb = sV + (j % NS) * C::kTile;
-          const uint32_t pa = tmem + kColS + (j % 2) * 64;
+          const uint32_t vb = sV + s * C::kTile, pa = tg + kColS + (jv % 2) * 64;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc::umma_bf16_ts(tmem + kColO, pa + kk * 8, tc::sdesc_sw128(vb + kk * 2048, C::kHalf, 1024), idPV,
-                             (i > 0 || kk > 0) ? 1u : 0u);
-          tc::umma_commit(&c.o_ready);
-          tc::umma_commit(&c.v_empty[j % NS]);
+            tc::umma_bf16_ts(tg, pa + kk * 8, tc::sdesc_sw128(vb + kk * 2048, C::kHalf, 1024), idPV,
+                             (!first || kk > 0) ? 1u : 0u);
+          tc::umma_commit(&b.o_ready);
+          tc::umma_commit(&c.v_empty[s]);
+          first = false;
+          ++jv;
         }
       }
       __syncwarp();
@@ -347,37 +389,46 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
       x = xe;
       if (x < x1) w.next(a, it);
     }
-  } else {
+  } else if (warp >= 4) {
     // ---------------- softmax warps ----------------
+    const int g = (warp - 4) / 4;
+    Group& b = c.g[g];
     const int quarter = warp & 3;                        // TMEM lane quarter of this warp
-    const int r = quarter * 32 + lane;                   // row of the item
-    const int tid = threadIdx.x - 64;                    // 0..127
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int tid = (threadIdx.x - 128) % 128;           // thread of the group
+    const int rt = quarter * 32 + lane;                  // row of the group's tile
+    const uint32_t tl = tmem + g * 256 + ((uint32_t)(quarter * 32) << 16);
     const float scale_log2 = a.scale_log2;
-    int n = 0, seg = 0;
+    int n = 0, seg = 0, j = 0, halves = 0;               // j: tiles of this group
     bool ok = true;
     for (long long x = x0; x < x1; ++seg) {
       const long long xe = min(x1, it.first + it.n_tiles);
       const int ta = (int)(x - it.first), tb = (int)(xe - it.first);
-      const bool live = quarter * 32 < it.rows;          // the warp has rows
+      const bool share = it.rows <= GR;
+      const int r0 = share ? 0 : g * GR, rows = min(GR, it.rows - r0);     // the group's rows
+      const int r = r0 + rt;
+      const bool row_ok = rt < rows;
+      const bool live = quarter * 32 < rows;             // the warp has rows
       int head, t;
-      row_of<false>(a, it, r < it.rows ? r : 0, head, t);
+      row_of<false>(a, it, row_ok ? r : 0, head, t);
       const size_t grow = ((size_t)it.b * a.Hq + head) * a.g.T + t;
       {
         // every product that read the previous Q has completed: its S was read below
         const uint4* qr = reinterpret_cast<const uint4*>(a.q + grow * D);
 #pragma unroll
         for (int ch = 0; ch < D / 8; ++ch) {
-          const uint4 v = r < it.rows ? __ldg(qr + ch) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(sm + C::kQ + (ch >> 3) * C::kQHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+          const uint4 v = row_ok ? __ldg(qr + ch) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(sm + C::kQ + g * C::kQTile + (ch >> 3) * C::kQHalf + rt * 128 +
+                                    (((ch & 7) ^ (rt & 7)) << 4)) = v;
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&c.q_full);
+        if (lane == 0) tc::mbar_arrive(&b.q_full);
       }
       float m_used = -INFINITY, l = 0.f;
+      bool first = true;                                 // no tile of the group in this segment yet
       for (int tile = ta; tile < tb; ++tile, ++n) {
-        if (ok) ok = warp_all(tc::mbar_wait(&c.s_full[n % 2], (n / 2) & 1, abort_flag, status));
+        if (share && (n & 1) != g) continue;
+        if (ok) ok = warp_all(tc::mbar_wait(&b.s_full[j % 2], (j / 2) & 1, abort_flag, status));
         if (!ok) continue;
         tc::tc_fence_after();
         const int pos0 = tile * kTileKeys;
@@ -385,12 +436,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
         const bool drafts = pos0 + kTileKeys > it.base;
         if (vm != ~0ull || (drafts && (a.mask || it.ql > 1))) {
           // mend the V tile: rows that are no keys become 0, non-finite drafted values are taken out
+          // (by both groups, alike, where both use the tile)
           ok = warp_all(tc::mbar_wait(&c.v_full[n % NS], (n / NS) & 1, abort_flag, status));
           if (!ok) continue;
           const int row = tid / 2;
           const bool key = (vm >> row) & 1;
           if (!key || (drafts && pos0 + row >= it.base)) {
-            bool found = false;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               const int ch = (tid & 1) * (D / 16) + i;
@@ -399,12 +450,16 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
               uint4 v = make_uint4(0, 0, 0, 0);
               if (key) {
                 v = *p;
-                found |= clear_nonfinite<F16>(v.x) | clear_nonfinite<F16>(v.y) | clear_nonfinite<F16>(v.z) |
-                         clear_nonfinite<F16>(v.w);
+                if (clear_nonfinite<F16>(v.x) | clear_nonfinite<F16>(v.y) | clear_nonfinite<F16>(v.z) |
+                    clear_nonfinite<F16>(v.w)) {
+                  // before the value goes: who finds it gone finds the flags set
+                  atomicOr(&c.flag[0][seg & 1], 1);
+                  atomicOr(&c.flag[1][seg & 1], 1);
+                  __threadfence_block();
+                }
               }
               *p = v;
             }
-            if (found) atomicOr(&c.flag[seg & 1], 1);
           }
           tc::fence_proxy_async_smem();
         }
@@ -412,12 +467,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
         uint32_t pk[32];
         if (live) {
           float s[64];
+          {
+            uint32_t v[64];
+            tc::tmem_ld64(tl + kColS + (j % 2) * 64, v);
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            uint32_t v[32];
-            tc::tmem_ld32(tl + kColS + (n % 2) * 64 + cc * 32, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[cc * 32 + i] = __uint_as_float(v[i]);
+            for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(v[i]);
           }
           float mx8[8];
 #pragma unroll
@@ -455,87 +509,136 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
           }
           l = l * alpha + ((sum0 + sum1) + (sum2 + sum3));
         }
-        if (n > 0) {
+        if (j > 0) {
           // the previous value product has landed: O may be rescaled, and the arrival below is
-          // for phase n
-          ok = warp_all(tc::mbar_wait(&c.o_ready, (n - 1) & 1, abort_flag, status));
+          // for phase j
+          ok = warp_all(tc::mbar_wait(&b.o_ready, (j - 1) & 1, abort_flag, status));
           if (!ok) continue;
           tc::tc_fence_after();
         }
         if (live) {
-          if (tile > ta && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
               uint32_t v[32];
-              tc::tmem_ld32(tl + kColO + cc * 32, v);
+              tc::tmem_ld32(tl + cc * 32, v);
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-              tc::tmem_st32(tl + kColO + cc * 32, v);
+              tc::tmem_st32(tl + cc * 32, v);
             }
           }
-          tc::tmem_st32(tl + kColS + (n % 2) * 64, pk);  // P over the S just read
+          tc::tmem_st32(tl + kColS + (j % 2) * 64, pk);  // P over the S just read
         }
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&c.p_full);
+        if (lane == 0) tc::mbar_arrive(&b.p_full);
+        first = false;
+        ++j;
       }
       // ---- result, or partial result ----
-      if (ok) ok = warp_all(tc::mbar_wait(&c.o_ready, (n - 1) & 1, abort_flag, status));
-      softmax_sync();                                    // the flag is complete
-      const int fixup = *(volatile int*)&c.flag[seg & 1];
-      const bool whole = ta == 0 && tb == it.n_tiles;
-      const size_t slot = 2 * (size_t)blockIdx.x + (ta == 0 ? 1 : 0);
-      if (ok && live) {
-        tc::tc_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (ok && j > 0) ok = warp_all(tc::mbar_wait(&b.o_ready, (j - 1) & 1, abort_flag, status));
+      tc::tc_fence_after();
+      const int par = halves & 1;
+      float f0 = first ? 0.f : 1.f, f1 = 0.f;            // weights of the two groups' states
+      if (share) {
+        ++halves;
+        if (g == 1) {
+          if (ok && live && !first) {
 #pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t v[32];
-          __syncwarp();
-          tc::tmem_ld32(tl + kColO + cc * 32, v);
-          if (r < it.rows && whole) {
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t v[32];
+              __syncwarp();
+              tc::tmem_ld32(tl + cc * 32, v);
+              if (row_ok) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              float y[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[i + e]) * inv;
-              if (fixup) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] += nonfinite_drafts<F16>(a, it, t, cc * 32 + i + e);
+                for (int i = 0; i < 8; ++i)
+                  *reinterpret_cast<uint4*>(half4(a, par, D, cc * 8 + i, rt)) =
+                      make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
               }
-              *reinterpret_cast<uint4*>(a.out + grow * D + cc * 32 + i) =
-                  make_uint4(pack_16<F16>(y[0], y[1]), pack_16<F16>(y[2], y[3]), pack_16<F16>(y[4], y[5]),
-                             pack_16<F16>(y[6], y[7]));
             }
-          } else if (r < it.rows) {
+          }
+          if (row_ok) *half_ml(a, par, rt) = make_float2(m_used, l);
+          __syncwarp();
+          tc::tc_fence_before();
+        }
+      }
+      // group 1's state and the flags are there (and no group is more than a segment ahead, whose
+      // flags are the other pair's)
+      both_sync();
+      if (share) {
+        if (g == 0 && row_ok) {
+          const float2 ml = __ldcg(half_ml(a, par, rt));
+          const float m = fmaxf(m_used, ml.x);
+          f0 = m_used == -INFINITY ? 0.f : ex2(m_used - m);
+          f1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+          l = l * f0 + ml.y * f1;
+          m_used = m;
+        }
+      }
+      if (!share || g == 0) {
+        const int fixup = *(volatile int*)&c.flag[g][seg & 1];
+        const bool whole = ta == 0 && tb == it.n_tiles;
+        const size_t slot = 2 * (size_t)blockIdx.x + (ta == 0 ? 1 : 0);
+        if (ok && live) {
+          const float inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(part4(a, slot, D, cc * 8 + i, r)) =
-                  make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t v[32];
+            __syncwarp();
+            tc::tmem_ld32(tl + cc * 32, v);
+            float y[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = f0 == 0.f ? 0.f : __uint_as_float(v[i]) * (f0 * inv);
+            if (f1 != 0.f) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 o1 = __ldcg(half4(a, par, D, cc * 8 + i, rt));
+                y[4 * i] = fmaf(o1.x, f1 * inv, y[4 * i]);
+                y[4 * i + 1] = fmaf(o1.y, f1 * inv, y[4 * i + 1]);
+                y[4 * i + 2] = fmaf(o1.z, f1 * inv, y[4 * i + 2]);
+                y[4 * i + 3] = fmaf(o1.w, f1 * inv, y[4 * i + 3]);
+              }
+            }
+            if (row_ok && whole) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                if (fixup) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) y[i + e] += nonfinite_drafts<F16>(a, it, t, cc * 32 + i + e);
+                }
+                *reinterpret_cast<uint4*>(a.out + grow * D + cc * 32 + i) =
+                    make_uint4(pack_16<F16>(y[i], y[i + 1]), pack_16<F16>(y[i + 2], y[i + 3]),
+                               pack_16<F16>(y[i + 4], y[i + 5]), pack_16<F16>(y[i + 6], y[i + 7]));
+              }
+            } else if (row_ok) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *part4(a, slot, D, cc * 8 + i, r) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            }
           }
-        }
-        if (r < it.rows) {
-          if (whole) {
-            if (a.lse)
-              a.lse[grow] = l == 0.f ? -INFINITY : (m_used - kShift + log2f(l)) * 0.69314718055994531f;
-          } else {
-            *reinterpret_cast<float2*>(a.part_ml + (slot * RT + r) * 2) = make_float2(m_used, l);
+          if (row_ok) {
+            if (whole) {
+              if (a.lse) a.lse[grow] = l == 0.f ? -INFINITY : (m_used - kShift + log2f(l)) * 0.69314718055994531f;
+            } else {
+              *reinterpret_cast<float2*>(a.part_ml + (slot * RT + r) * 2) = make_float2(m_used, l);
+            }
           }
+          __syncwarp();
+          tc::tc_fence_before();
         }
-        __syncwarp();
-        tc::tc_fence_before();
+        if (!whole) {
+          // ---- arrival; the last CTA joins the parts ----
+          if (tid == 0 && fixup) *(volatile int32_t*)(a.part_flag + 2 * slot + g) = 1;
+          if (tid == 0 && !fixup) *(volatile int32_t*)(a.part_flag + 2 * slot + g) = 0;
+          group_sync(g);
+          const Parts<false, RT> parts(w, it);
+          if (tid == 0) c.last[g] = arrive_part(a.arrived + 2 * parts.c1 + g, parts.n);
+          group_sync(g);
+          if (c.last[g]) join_rows<D, F16>(a, it, parts, r0, rows, tid, ok);
+        }
       }
-      if (!whole) {
-        // ---- arrival; the last CTA joins the parts ----
-        if (tid == 0) a.part_flag[slot] = fixup;
-        softmax_sync();
-        const Parts<false, RT> parts(w, it);
-        if (tid == 0) c.last = arrive_part(a.arrived + parts.c1, parts.n);
-        softmax_sync();
-        if (c.last) join_rows<D, F16>(a, it, parts, tid, ok);
-      }
-      softmax_sync();
-      if (tid == 0) c.flag[seg & 1] = 0;                 // next used two segments on, behind barriers
+      group_sync(g);
+      if (tid == 0) c.flag[g][seg & 1] = 0;              // next used two segments on, behind barriers
       x = xe;
       if (x < x1) w.next(a, it);
     }
@@ -550,12 +653,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attend_tc_kernel(
     wait_prepared();                             // in every CTA: this kernel's end is that one's, too
     if (c.status) atomicOr(a.dev_status, c.status);
   }
-  if (warp == 1) {
-    if (lane == 0 && mma_issued) {
-      tc::umma_commit(&c.done);
-      tc::mbar_wait_timed(&c.done, 0);
-    }
-    __syncwarp();
+  if ((warp == 1 || warp == 2) && lane == 0 && mma_issued) {
+    // every MMA this thread issued has completed once this commit arrives
+    tc::umma_commit(&c.g[warp - 1].done);
+    tc::mbar_wait_timed(&c.g[warp - 1].done, 0);
+  }
+  __syncthreads();
+  if (warp == 3) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
@@ -571,7 +675,7 @@ static cudaError_t attend_tc_t(const bsa_cache_shape& s, const PagedArgs& a, con
     return cudaErrorInvalidValue;
   auto kern = paged_attend_tc_kernel<D, F16>;
   constexpr size_t smem = smem_bytes<D>();
-  static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(smem <= 227 * 1024, "paged attend shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   e = launch_paged_prepare(a, st);

@@ -39,8 +39,11 @@ struct PagedArgs {
   float* lse;
   float* part_o;                    // [2 * n_cta][RT][d]
   float* part_ml;                   // [2 * n_cta][RT][2]
-  int32_t* part_flag;               // [2 * n_cta]
-  int32_t* arrived;                 // [n_cta]: parts of the item that ends in the CTA's share
+  int32_t* part_flag;               // [2 * n_cta], two each on tcgen05 (a group's rows)
+  int32_t* arrived;                 // [n_cta], two each on tcgen05: parts of the item that ends in the CTA's share
+  int n_arrived;
+  float* half_o;                    // tcgen05: [2 * n_cta][128][d], group 1's states
+  float* half_ml;                   // ... [2 * n_cta][128][2]
   int32_t* dev_status;
   int n_cta;
 };
@@ -60,7 +63,7 @@ struct Item {
 // How far a share may shrink: below this many tiles per CTA the arrival and the join cost more time
 // than the shorter share saves.
 template <int RT>
-constexpr int kMinTiles = RT == 128 ? 2 : 4;
+constexpr int kMinTiles = RT == 256 ? 2 : 4;
 
 template <bool LIST, int RT>
 struct Walk {
@@ -316,7 +319,7 @@ inline cudaLaunchConfig_t beside(cudaLaunchAttribute* at, unsigned grid, unsigne
 cudaError_t launch_paged_attend_mma(const bsa_cache_shape& s, PagedArgs a, const void* k, const void* v,
                                     cudaStream_t st);
 
-// The same on tcgen05 (row tiles of 128, whole cache only; a.n_cta: two per SM).
+// The same on tcgen05 (row tiles of 256, whole cache only).
 cudaError_t launch_paged_attend_tc(const bsa_cache_shape& s, const PagedArgs& a, const void* k, const void* v,
                                    cudaStream_t st);
 

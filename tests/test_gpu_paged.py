@@ -94,6 +94,43 @@ def test_chain(T):
     _run_tree(31, lens=[T, T + 1, T + 500], qls=[T, min(T, 3), T], T=T, Hq=8, Hkv=2, d=128, page=64)
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,page,d,dtype,B", [
+    (1, 8, 4, 16, 128, "bf16", 40), (6, 4, 2, 16, 64, "fp16", 40), (24, 4, 2, 64, 128, "bf16", 40),
+    (70, 8, 4, 32, 64, "bf16", 20), (70, 4, 2, 128, 128, "fp16", 20), (9, 8, 4, 16, 64, "bf16", 30)])
+def test_many_tiles_per_share(T, Hq, Hkv, page, d, dtype, B):
+    """Enough work that every SM walks many tiles and several items: the rings wrap, and segments
+    begin and end inside shares. Sampled sequences against the oracle, the status for all."""
+    rng = random.Random(7)
+    qls = [rng.choice([T, T, max(1, T // 2), 1]) for _ in range(B)]
+    lens = [ql + rng.choice([0, 900, 2500, 4000]) + rng.randint(0, 130) for ql in qls]
+    cache = make_cache(33, lens=lens, max_pages=-(-max(lens) // page), page=page, Hkv=Hkv, d=d, dtype=dtype,
+                       garbage=float("nan"))
+    q = torch.randn(B, Hq, T, d, generator=torch.Generator().manual_seed(34)).to(DT[dtype])
+    out, lse, st = paged.attend_tree(q.cuda(), cache, q_len=_i32(qls))
+    out2, lse2, st2 = paged.attend_tree(q.cuda(), cache, q_len=_i32(qls))
+    assert int(st) == 0 and int(st2) == 0
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)              # bit for bit
+    assert torch.isfinite(out.float()).all()
+    k, v, table, qn = cache.k[0].cpu(), cache.v[0].cpu(), cache.page_table.cpu().tolist(), f8(q)
+    go, gl = f8(out), f8(lse)
+    for b in range(0, B, 4):
+        n, ql, G = lens[b], qls[b], Hq // Hkv
+        pages = torch.tensor(table[b][:-(-n // page)])
+        for h in range(Hkv):
+            kr, vr = (f8(x[pages, h].reshape(-1, d)[:n]) for x in (k, v))
+            qh = qn[b, h * G:(h + 1) * G, :ql].reshape(G * ql, d)
+            see = np.ones((ql, n), bool)
+            see[:, n - ql:] = np.tril(np.ones((ql, ql), bool))
+            z = np.where(np.tile(see, (G, 1)), qh @ kr.T * scale_of(d), -np.inf)
+            m = z.max(1, keepdims=True)
+            p = np.exp(z - m)
+            ro, rl = p @ vr / p.sum(1, keepdims=True), (m + np.log(p.sum(1, keepdims=True)))[:, 0]
+            km, vm = np.abs(kr).max(), np.abs(vr).max()
+            check(go[b, h * G:(h + 1) * G, :ql].reshape(-1, d), ro,
+                  out_tolerance(ro, qh, km, vm, d, scale_of(d), dtype, 16 if G * T <= 16 else 8), (b, h))
+            check(gl[b, h * G:(h + 1) * G, :ql].reshape(-1), rl, lse_tolerance(rl, qh, km, d, scale_of(d), n), (b, h))
+
+
 def test_mask_that_leaves_rows_empty():
     see = np.zeros((2, 6, 6), bool)
     see[0, 2, 4] = see[0, 3, 0] = True          # any mask, not ancestors alone; other rows see nothing
