@@ -93,8 +93,6 @@ struct AttendWs {
   float* part_ml;
   int32_t* part_flag;
   int32_t* arrived;
-  float* half_o;
-  float* half_ml;
   int n_cta, n_arrived;
   bool tc;
   size_t bytes;
@@ -115,10 +113,6 @@ AttendWs attend_ws(const bsa_cache_shape& s, int Hq, int T, bool list, void* bas
   w.part_ml = (float*)(p + off); off += align256(slots * rt * 2 * 4);
   w.part_flag = (int32_t*)(p + off); off += align256(2 * slots * 4);
   w.arrived = (int32_t*)(p + off); off += align256((size_t)w.n_arrived * 4);
-  if (tc) {
-    w.half_o = (float*)(p + off); off += align256(slots * 128 * s.d * 4);
-    w.half_ml = (float*)(p + off); off += align256(slots * 128 * 2 * 4);
-  }
   w.bytes = off;
   return w;
 }
@@ -173,8 +167,6 @@ bsa_status attend(const bsa_cache_shape* s, int slots, int max_pages, int Hq, in
   a.part_flag = w.part_flag;
   a.arrived = w.arrived;
   a.n_arrived = w.n_arrived;
-  a.half_o = w.half_o;
-  a.half_ml = w.half_ml;
   a.dev_status = dev_status;
   a.n_cta = w.n_cta;
   cudaStream_t cs = (cudaStream_t)stream;

@@ -750,7 +750,8 @@ cudaError_t launch_select_pages(const bsa_cache_shape& s, const CacheGeom& g, co
   auto kern = kmax_abs ? (f16 ? page_list_kernel<true, true> : page_list_kernel<true, false>)
                        : (f16 ? page_list_kernel<false, true> : page_list_kernel<false, false>);
   const size_t smem = (size_t)g.max_pages * 4;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemSet sets[4];                       // (the most that any table needs)
+  e = allow_smem((const void*)kern, kMaxTablePages * 4, sets[(kmax_abs ? 2 : 0) + f16]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((long long)g.slots * g.Hkv * g.T));

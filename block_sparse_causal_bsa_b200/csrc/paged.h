@@ -58,7 +58,12 @@ cudaError_t launch_tree_mask(int B, int T, const int32_t* parents, const int32_t
 
 namespace bsa {
 
-int sm_count();                        // of the current device
+// Of the current device; both are asked once per device (a step makes many of these calls).
+int sm_count();
+struct SmemSet {                       // one per kernel, static
+  unsigned long long done[4] = {};
+};
+cudaError_t allow_smem(const void* kernel, size_t bytes, SmemSet& set);
 
 // Page scores into scores [slots*Hkv*T][max_pages], then the lists. kmax_abs [slots*Hkv][max_pages]
 // (workspace): the scores are fp32 estimates, and what they leave open is decided in fp64; null: the

@@ -29,6 +29,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "paged_work.cuh"
 #include "tc_common.cuh"
 
@@ -140,10 +142,10 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
   const int np = parts.n;
   static_assert(sizeof(c.ml) >= kMaxPartsCtas * RT * sizeof(float2), "room for every part");
   for (int i = tid; i < np * RT; i += 32 * kWarps)
-    c.ml[i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (parts.slot(i / RT) * RT + i % RT) * 2));
+    c.ml[i] = read_l2(reinterpret_cast<const float2*>(a.part_ml + (parts.slot(i / RT) * RT + i % RT) * 2));
   if (!LIST)
     for (int i = tid; i < np; i += 32 * kWarps)
-      if (__ldcg(a.part_flag + parts.slot(i))) atomicOr(&c.last, 2);
+      if (read_l2(a.part_flag + parts.slot(i))) atomicOr(&c.last, 2);
   float4 v[kU];
   auto read = [&](int i, int p0) {
     const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
@@ -151,7 +153,7 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
     for (int u = 0; u < kU; ++u) {
       v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (p0 + u < np && r < it.rows)
-        v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (parts.slot(p0 + u) * RT + r) * D + d4));
+        v[u] = read_l2(reinterpret_cast<const float4*>(a.part_o + (parts.slot(p0 + u) * RT + r) * D + d4));
     }
   };
   if (tid < RT * (D / 4)) read(tid, 0);
@@ -572,11 +574,28 @@ __global__ void __launch_bounds__(256) paged_prepare_kernel(CacheGeom g, int n, 
 // host
 
 int sm_count() {
+  static std::atomic<int> count[256];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 148;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 256) return 148;
+  n = count[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    count[dev].store(n, std::memory_order_relaxed);
+  }
   return n;
+}
+
+cudaError_t allow_smem(const void* kernel, size_t bytes, SmemSet& set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev < 256;
+  unsigned long long* word = &set.done[(dev & 255) / 64];
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (known && (__atomic_load_n(word, __ATOMIC_RELAXED) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && known) __atomic_fetch_or(word, bit, __ATOMIC_RELAXED);
+  return e;
 }
 
 cudaError_t launch_paged_prepare(const PagedArgs& a, cudaStream_t st) {
@@ -595,7 +614,8 @@ static cudaError_t attend_t(const bsa_cache_shape& s, const PagedArgs& a, const 
   auto kern = paged_attend_kernel<D, RT, F16, LIST>;
   constexpr size_t smem = smem_bytes<D, RT>();
   static_assert(smem <= 227 * 1024, "paged attend shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemSet set;
+  cudaError_t e = allow_smem((const void*)kern, smem, set);
   if (e != cudaSuccess) return e;
   e = launch_paged_prepare(a, st);
   if (e != cudaSuccess) return e;

@@ -19,8 +19,9 @@
 //               by more than 2^8), P in 16 bits over the S just read; O / l or the partial result at the end
 //               of a segment. Warps whose rows are all past the item's skip the arithmetic.
 // Items of more than 128 rows: group 1 takes rows 128 and up, both groups every tile. Items of up to
-// 128 rows: both groups take the same rows and every other tile, and group 0 adds up the two states at
-// the end of a segment (group 1 leaves its own in the workspace, two areas in turn).
+// 128 rows: both groups take the same rows and every other tile, and at the end of a segment each adds
+// up the two states for half the channels (a row sits in the same TMEM lane in both groups, so a warp
+// reads the other group's output where it is).
 // P is rounded to 16 bits, a relative 2^-9 (bf16) or 2^-12 (fp16) per weight, within the rounding of the
 // output; sums and maxima are fp32. For fp16, weights carry a factor 2^7: with the maximum up to 2^8
 // stale they stay below 2^15, and weights down to 2^-31 of the largest still count.
@@ -111,65 +112,72 @@ __device__ __forceinline__ uint64_t draft_window(const PagedArgs& a, int b, int 
 __device__ __forceinline__ float4* part4(const PagedArgs& a, size_t slot, int D, int d4, int r) {
   return reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + d4) * RT + r;
 }
-// Group 1's state of a segment whose tiles the groups share: area `par` of the CTA.
-__device__ __forceinline__ float4* half4(const PagedArgs& a, int par, int D, int d4, int r) {
-  return reinterpret_cast<float4*>(a.half_o) + ((2 * (size_t)blockIdx.x + par) * (D / 4) + d4) * GR + r;
-}
-__device__ __forceinline__ float2* half_ml(const PagedArgs& a, int par, int r) {
-  return reinterpret_cast<float2*>(a.half_ml) + (2 * (size_t)blockIdx.x + par) * GR + r;
-}
-
-// Joins the parts of a group's rows [r0, r0 + rows) of an item, its four softmax warps: 128 / R threads per
-// row, R the rows rounded up to whole warps; eight reads of 16 bytes in flight per thread.
+// Joins the parts of the rows [r0, r0 + rows) of an item, channels 4 d0 .. 4 d1, one group: 128 / R
+// threads per row, R the rows rounded up to whole warps, each a run of channels; sixteen reads of 16
+// bytes in flight per thread.
 template <int D, bool F16>
 __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const Parts<false, RT>& parts, int r0,
-                                       int rows, int tid, bool ok) {
+                                       int rows, int d0, int d1, int flag_at, int tid, bool ok) {
   constexpr float kShift = F16 ? 7.f : 0.f;
   constexpr int kU = 8;
   const int np = parts.n, R = (rows + 31) / 32 * 32;
   const int groups = 128 / R, dg = tid / R;                    // (R = 96: one group, 32 threads idle)
   if (dg >= groups || tid % R >= rows) return;
   const int r = r0 + tid % R;
+  const int per = (d1 - d0 + groups - 1) / groups;
+  const int da = d0 + dg * per, db = min(da + per, d1);
+  auto ml_of = [&](int i) { return reinterpret_cast<const float2*>(a.part_ml + (parts.slot(i) * RT + r) * 2); };
   float mx = -INFINITY, ls = 0.f;
   int flag = 0;
-#pragma unroll 8
+#pragma unroll 4
   for (int i = 0; i < np; ++i) {
-    mx = fmaxf(mx, __ldcg(a.part_ml + (parts.slot(i) * RT + r) * 2));
-    flag |= __ldcg(a.part_flag + 2 * parts.slot(i) + (r0 ? 1 : 0));
+    mx = fmaxf(mx, read_l2(ml_of(i)).x);
+    flag |= read_l2(a.part_flag + 2 * parts.slot(i) + flag_at);
   }
   int head, t;
   row_of<false>(a, it, r, head, t);
   const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
-  for (int d0 = dg; d0 < D / 4; d0 += groups * kU) {
+  for (int dc = da; dc < db; dc += kU) {
     float4 acc[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     ls = 0.f;
-#pragma unroll 2
-    for (int i = 0; i < np; ++i) {
-      const size_t slot = parts.slot(i);
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (slot * RT + r) * 2));
-      float4 v[kU];
+    for (int i = 0; i < np; i += 2) {
+      const int i1 = min(i + 1, np - 1);                       // (the odd last part counts once)
+      const size_t s0 = parts.slot(i), s1 = parts.slot(i1);
+      const float2 m0 = read_l2(ml_of(i)), m1 = read_l2(ml_of(i1));
+      float4 v[kU], w[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (d0 + u * groups < D / 4) v[u] = __ldcg(part4(a, slot, D, d0 + u * groups, r));
+        const int d4 = min(dc + u, db - 1);
+        v[u] = read_l2(part4(a, s0, D, d4, r));
+        w[u] = read_l2(part4(a, s1, D, d4, r));
       }
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
-      ls += ml.y * f;
+      const float f = m0.x == -INFINITY ? 0.f : ex2(m0.x - mx);
+      const float h = m1.x == -INFINITY || i1 == i ? 0.f : ex2(m1.x - mx);
+      ls += m0.y * f + m1.y * h;
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        acc[u].x = fmaf(v[u].x, f, acc[u].x);
-        acc[u].y = fmaf(v[u].y, f, acc[u].y);
-        acc[u].z = fmaf(v[u].z, f, acc[u].z);
-        acc[u].w = fmaf(v[u].w, f, acc[u].w);
+        // (a weight of 0 must not meet what an empty part holds)
+        if (f != 0.f) {
+          acc[u].x = fmaf(v[u].x, f, acc[u].x);
+          acc[u].y = fmaf(v[u].y, f, acc[u].y);
+          acc[u].z = fmaf(v[u].z, f, acc[u].z);
+          acc[u].w = fmaf(v[u].w, f, acc[u].w);
+        }
+        if (h != 0.f) {
+          acc[u].x = fmaf(w[u].x, h, acc[u].x);
+          acc[u].y = fmaf(w[u].y, h, acc[u].y);
+          acc[u].z = fmaf(w[u].z, h, acc[u].z);
+          acc[u].w = fmaf(w[u].w, h, acc[u].w);
+        }
       }
     }
     const float inv = ls == 0.f ? 0.f : 1.f / ls;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int d4 = d0 + u * groups;
-      if (d4 >= D / 4) break;
+      const int d4 = dc + u;
+      if (d4 >= db) break;
       float y[4] = {acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv};
       if (flag) {
 #pragma unroll
@@ -180,7 +188,7 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
             make_uint2(pack_16<F16>(y[0], y[1]), pack_16<F16>(y[2], y[3]));
     }
   }
-  if (ok && dg == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
+  if (ok && da == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
 }
 
 }  // namespace
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
     const int rt = quarter * 32 + lane;                  // row of the group's tile
     const uint32_t tl = tmem + g * 256 + ((uint32_t)(quarter * 32) << 16);
     const float scale_log2 = a.scale_log2;
-    int n = 0, seg = 0, j = 0, halves = 0;               // j: tiles of this group
+    int n = 0, seg = 0, j = 0;                           // j: tiles of this group
     bool ok = true;
     for (long long x = x0; x < x1; ++seg) {
       const long long xe = min(x1, it.first + it.n_tiles);
@@ -538,106 +546,98 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
       // ---- result, or partial result ----
       if (ok && j > 0) ok = warp_all(tc::mbar_wait(&b.o_ready, (j - 1) & 1, abort_flag, status));
       tc::tc_fence_after();
-      const int par = halves & 1;
-      float f0 = first ? 0.f : 1.f, f1 = 0.f;            // weights of the two groups' states
+      const bool whole = ta == 0 && tb == it.n_tiles;
+      const size_t slot = 2 * (size_t)blockIdx.x + (ta == 0 ? 1 : 0);
+      constexpr int kCh = D / 32;                        // pieces of 32 channels
+      const int c0 = share ? g * (kCh / 2) : 0, c1 = share ? c0 + kCh / 2 : kCh;     // the group's
+      auto tail_sync = [&]() {
+        if (share) both_sync();
+        else group_sync(g);
+      };
+      float f0 = first ? 0.f : 1.f, f1 = 0.f;            // weights of the group's state and of the other's
       if (share) {
-        ++halves;
-        if (g == 1) {
-          if (ok && live && !first) {
+        // maximum and sum, over the S that was read
+        uint32_t v[16];
+        v[0] = __float_as_uint(m_used);
+        v[1] = __float_as_uint(l);
 #pragma unroll
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t v[32];
-              __syncwarp();
-              tc::tmem_ld32(tl + cc * 32, v);
-              if (row_ok) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<uint4*>(half4(a, par, D, cc * 8 + i, rt)) =
-                      make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-              }
-            }
-          }
-          if (row_ok) *half_ml(a, par, rt) = make_float2(m_used, l);
-          __syncwarp();
-          tc::tc_fence_before();
-        }
+        for (int i = 2; i < 16; ++i) v[i] = 0u;
+        tc::tmem_st16(tl + kColS, v);
       }
-      // group 1's state and the flags are there (and no group is more than a segment ahead, whose
-      // flags are the other pair's)
+      tc::tc_fence_before();
+      // the flags and states are there (and no group is more than a segment ahead, whose flags are the
+      // other pair's)
       both_sync();
+      tc::tc_fence_after();
+      const uint32_t other = tl - g * 256 + (1 - g) * 256;
       if (share) {
-        if (g == 0 && row_ok) {
-          const float2 ml = __ldcg(half_ml(a, par, rt));
-          const float m = fmaxf(m_used, ml.x);
-          f0 = m_used == -INFINITY ? 0.f : ex2(m_used - m);
-          f1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-          l = l * f0 + ml.y * f1;
-          m_used = m;
-        }
+        uint32_t v[16];
+        tc::tmem_ld16(other + kColS, v);
+        const float mo = __uint_as_float(v[0]);
+        const float m = fmaxf(m_used, mo);
+        f0 = m_used == -INFINITY ? 0.f : ex2(m_used - m);
+        f1 = mo == -INFINITY ? 0.f : ex2(mo - m);
+        l = l * f0 + __uint_as_float(v[1]) * f1;
+        m_used = m;
       }
-      if (!share || g == 0) {
-        const int fixup = *(volatile int*)&c.flag[g][seg & 1];
-        const bool whole = ta == 0 && tb == it.n_tiles;
-        const size_t slot = 2 * (size_t)blockIdx.x + (ta == 0 ? 1 : 0);
-        if (ok && live) {
-          const float inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+      const int fixup = *(volatile int*)&c.flag[g][seg & 1];
+      if (ok && live) {
+        const float inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
 #pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t v[32];
-            __syncwarp();
-            tc::tmem_ld32(tl + cc * 32, v);
-            float y[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = f0 == 0.f ? 0.f : __uint_as_float(v[i]) * (f0 * inv);
-            if (f1 != 0.f) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 o1 = __ldcg(half4(a, par, D, cc * 8 + i, rt));
-                y[4 * i] = fmaf(o1.x, f1 * inv, y[4 * i]);
-                y[4 * i + 1] = fmaf(o1.y, f1 * inv, y[4 * i + 1]);
-                y[4 * i + 2] = fmaf(o1.z, f1 * inv, y[4 * i + 2]);
-                y[4 * i + 3] = fmaf(o1.w, f1 * inv, y[4 * i + 3]);
-              }
-            }
-            if (row_ok && whole) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                if (fixup) {
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) y[i + e] += nonfinite_drafts<F16>(a, it, t, cc * 32 + i + e);
-                }
-                *reinterpret_cast<uint4*>(a.out + grow * D + cc * 32 + i) =
-                    make_uint4(pack_16<F16>(y[i], y[i + 1]), pack_16<F16>(y[i + 2], y[i + 3]),
-                               pack_16<F16>(y[i + 4], y[i + 5]), pack_16<F16>(y[i + 6], y[i + 7]));
-              }
-            } else if (row_ok) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *part4(a, slot, D, cc * 8 + i, r) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-            }
-          }
-          if (row_ok) {
-            if (whole) {
-              if (a.lse) a.lse[grow] = l == 0.f ? -INFINITY : (m_used - kShift + log2f(l)) * 0.69314718055994531f;
-            } else {
-              *reinterpret_cast<float2*>(a.part_ml + (slot * RT + r) * 2) = make_float2(m_used, l);
-            }
-          }
+        for (int ci = 0; ci < kCh; ++ci) {
+          if (ci >= c1 - c0) break;
+          const int cc = c0 + ci;
+          uint32_t v[32];
           __syncwarp();
-          tc::tc_fence_before();
+          tc::tmem_ld32(tl + cc * 32, v);
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = f0 == 0.f ? 0.f : __uint_as_float(v[i]) * (f0 * inv);
+          if (share) {
+            tc::tmem_ld32(other + cc * 32, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (f1 != 0.f) y[i] = fmaf(__uint_as_float(v[i]), f1 * inv, y[i]);
+          }
+          if (row_ok && whole) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              if (fixup) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[i + e] += nonfinite_drafts<F16>(a, it, t, cc * 32 + i + e);
+              }
+              *reinterpret_cast<uint4*>(a.out + grow * D + cc * 32 + i) =
+                  make_uint4(pack_16<F16>(y[i], y[i + 1]), pack_16<F16>(y[i + 2], y[i + 3]),
+                             pack_16<F16>(y[i + 4], y[i + 5]), pack_16<F16>(y[i + 6], y[i + 7]));
+            }
+          } else if (row_ok) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *part4(a, slot, D, cc * 8 + i, r) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
         }
-        if (!whole) {
-          // ---- arrival; the last CTA joins the parts ----
-          if (tid == 0 && fixup) *(volatile int32_t*)(a.part_flag + 2 * slot + g) = 1;
-          if (tid == 0 && !fixup) *(volatile int32_t*)(a.part_flag + 2 * slot + g) = 0;
-          group_sync(g);
-          const Parts<false, RT> parts(w, it);
-          if (tid == 0) c.last[g] = arrive_part(a.arrived + 2 * parts.c1 + g, parts.n);
-          group_sync(g);
-          if (c.last[g]) join_rows<D, F16>(a, it, parts, r0, rows, tid, ok);
+        if (row_ok && c0 == 0) {
+          if (whole) {
+            if (a.lse) a.lse[grow] = l == 0.f ? -INFINITY : (m_used - kShift + log2f(l)) * 0.69314718055994531f;
+          } else {
+            *reinterpret_cast<float2*>(a.part_ml + (slot * RT + r) * 2) = make_float2(m_used, l);
+          }
         }
+        __syncwarp();
+        tc::tc_fence_before();
       }
-      group_sync(g);
+      if (!whole) {
+        // ---- arrival; the last CTA joins the parts ----
+        const int at = share ? 0 : g;
+        const bool lead = tid == 0 && (!share || g == 0);
+        if (lead) a.part_flag[2 * slot + at] = fixup;
+        tail_sync();
+        const Parts<false, RT> parts(w, it);
+        if (lead) c.last[at] = arrive_part(a.arrived + 2 * parts.c1 + at, parts.n);
+        tail_sync();
+        if (c.last[at]) join_rows<D, F16>(a, it, parts, r0, rows, c0 * 8, c1 * 8, at, tid, ok);
+      }
+      tail_sync();                                       // Q, the states and the flags may be written again
       if (tid == 0) c.flag[g][seg & 1] = 0;              // next used two segments on, behind barriers
       x = xe;
       if (x < x1) w.next(a, it);
@@ -676,7 +676,8 @@ static cudaError_t attend_tc_t(const bsa_cache_shape& s, const PagedArgs& a, con
   auto kern = paged_attend_tc_kernel<D, F16>;
   constexpr size_t smem = smem_bytes<D>();
   static_assert(smem <= 227 * 1024, "paged attend shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemSet set;
+  cudaError_t e = allow_smem((const void*)kern, smem, set);
   if (e != cudaSuccess) return e;
   e = launch_paged_prepare(a, st);
   if (e != cudaSuccess) return e;

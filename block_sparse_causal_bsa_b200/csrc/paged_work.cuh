@@ -42,8 +42,6 @@ struct PagedArgs {
   int32_t* part_flag;               // [2 * n_cta], two each on tcgen05 (a group's rows)
   int32_t* arrived;                 // [n_cta], two each on tcgen05: parts of the item that ends in the CTA's share
   int n_arrived;
-  float* half_o;                    // tcgen05: [2 * n_cta][128][d], group 1's states
-  float* half_ml;                   // ... [2 * n_cta][128][2]
   int32_t* dev_status;
   int n_cta;
 };
@@ -272,6 +270,24 @@ __device__ __noinline__ float nonfinite_drafts(const PagedArgs& a, const Item& i
     if (!isfinite(x)) s += x;
   }
   return s;
+}
+
+// Reads from L2 of what other SMs wrote in this kernel. (volatile: they stay behind the barrier or
+// the atomic that says it is there.)
+__device__ __forceinline__ float4 read_l2(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 read_l2(const float2* p) {
+  float2 v;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ int read_l2(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
 }
 
 // What waits for the preparing kernel (counters and *dev_status are set when it returns).

@@ -28,7 +28,7 @@ from typing import Optional
 import torch
 
 from .binding import (BSA_BF16, BSA_ERR_INVALID_ARG, BSA_ERR_UNSUPPORTED, BSA_F16, BsaError, CacheShape,
-                      PageSelectParams, _check, _empty_bytes, lib)
+                      PageSelectParams, _check, lib)
 
 _DTYPES = {torch.bfloat16: BSA_BF16, torch.float16: BSA_F16}
 
@@ -64,6 +64,9 @@ class PagedCache:
                    seq_len=torch.zeros(slots, **i32), refs=torch.zeros(n_pages, **i32))
 
     def __post_init__(self):
+        self.shape()
+
+    def _check(self):
         if self.k.dim() != 5 or self.k.shape != self.v.shape:
             _bad("k and v must be [layers, n_pages, Hkv, page, d]")
         L, P, H, page, d = self.k.shape
@@ -91,9 +94,31 @@ class PagedCache:
     def max_pages(self) -> int:
         return self.page_table.shape[1]
 
-    def shape(self) -> CacheShape:
-        _, P, H, page, d = self.k.shape
-        return CacheShape(P, H, page, d, _DTYPES[self.k.dtype])
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if not name.startswith("_"):             # what is derived from the tensors is derived anew
+            object.__setattr__(self, "_shape", None)
+            object.__setattr__(self, "_bytes", {})
+
+    def shape(self):
+        """The C shape (by reference), kept until a tensor of the cache is replaced."""
+        if self._shape is None:
+            self._check()
+            _, P, H, page, d = self.k.shape
+            self._shape = ctypes.byref(CacheShape(P, H, page, d, _DTYPES[self.k.dtype]))
+        return self._shape
+
+    def workspace_bytes(self, call: str, Hq: int, T: int) -> int:
+        n = self._bytes.get((call, Hq, T))
+        if n is None:
+            n = getattr(lib(), f"bsa_{call}_workspace_bytes")(self.shape(), self.slots, self.max_pages, Hq, T)
+            if n == 0:
+                _bad(lib().bsa_last_error().decode(), BSA_ERR_UNSUPPORTED)
+            self._bytes[(call, Hq, T)] = n
+        return n
+
+    def _scratch(self, nbytes: int) -> torch.Tensor:
+        return self.refs.new_empty((nbytes + 3) // 4)
 
     def _layer(self, layer: int):
         L, P, H, page, d = self.k.shape
@@ -104,6 +129,7 @@ class PagedCache:
                 self.bounds.data_ptr() + 2 * step if self.bounds is not None else None)
 
     def _table(self):
+        self.shape()
         return self.slots, self.max_pages, self.k.shape[1], self.k.shape[3]
 
 
@@ -159,8 +185,8 @@ class _On:
         return False
 
 
-def _status(device):
-    return torch.empty(1, dtype=torch.int32, device=device)
+def _status(like):
+    return like.new_empty(1)
 
 
 def _qlen(cache, q_len):
@@ -172,7 +198,7 @@ def fork(cache: PagedCache, parent: torch.Tensor, *, stream=None) -> torch.Tenso
     pages. Returns the status."""
     p = _tensor("parent", parent, (cache.slots,), torch.int32, cache.device)
     with _On(cache.device, stream) as s:
-        st = _status(cache.device)
+        st = _status(cache.refs)
         _check(lib().bsa_pages_fork(*cache._table(), cache.page_table.data_ptr(), cache.seq_len.data_ptr(),
                                     cache.refs.data_ptr(), p, st.data_ptr(), s))
     return st
@@ -183,8 +209,8 @@ def resize(cache: PagedCache, new_len: torch.Tensor, *, stream=None):
     pages. Returns (pairs [slots, 2] for copy_pages, free pages left, status)."""
     n = _tensor("new_len", new_len, (cache.slots,), torch.int32, cache.device)
     with _On(cache.device, stream) as s:
-        st, n_free = _status(cache.device), _status(cache.device)
-        pairs = torch.empty(cache.slots, 2, dtype=torch.int32, device=cache.device)
+        st, n_free = _status(cache.refs), _status(cache.refs)
+        pairs = cache.refs.new_empty(cache.slots, 2)
         _check(lib().bsa_pages_resize(*cache._table(), cache.page_table.data_ptr(),
                                       cache.seq_len.data_ptr(), cache.refs.data_ptr(), n, pairs.data_ptr(),
                                       n_free.data_ptr(), st.data_ptr(), s))
@@ -200,10 +226,10 @@ def copy_pages(cache: PagedCache, pairs: torch.Tensor, *, layer: int = 0, stream
     k, v, b = cache._layer(layer)
     shape = cache.shape()
     with _On(cache.device, stream) as s:
-        st = _status(cache.device)
+        st = _status(cache.refs)
         if pairs.shape[0] == 0:
             return st.zero_()
-        _check(lib().bsa_pages_copy(ctypes.byref(shape), k, v, b, p, pairs.shape[0], st.data_ptr(), s))
+        _check(lib().bsa_pages_copy(shape, k, v, b, p, pairs.shape[0], st.data_ptr(), s))
     return st
 
 
@@ -221,8 +247,8 @@ def append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, *, q_len
     k, v, b = cache._layer(layer)
     shape = cache.shape()
     with _On(cache.device, stream) as s:
-        st = _status(cache.device)
-        _check(lib().bsa_cache_append(ctypes.byref(shape), cache.slots, cache.max_pages, T, kn, vn, k, v, b,
+        st = _status(cache.refs)
+        _check(lib().bsa_cache_append(shape, cache.slots, cache.max_pages, T, kn, vn, k, v, b,
                                       cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
                                       st.data_ptr(), s))
     return st
@@ -241,8 +267,8 @@ def compact(cache: PagedCache, keep: torch.Tensor, n_keep: torch.Tensor, *, q_le
     k, v, b = cache._layer(layer)
     shape = cache.shape()
     with _On(cache.device, stream) as s:
-        st = _status(cache.device)
-        _check(lib().bsa_cache_compact(ctypes.byref(shape), cache.slots, cache.max_pages, T, kp, nk, k, v, b,
+        st = _status(cache.refs)
+        _check(lib().bsa_cache_compact(shape, cache.slots, cache.max_pages, T, kp, nk, k, v, b,
                                        cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
                                        st.data_ptr(), s))
     return st
@@ -258,7 +284,7 @@ def tree_mask(parents: torch.Tensor, *, q_len=None, stream=None):
     p = _tensor("parents", parents, (B, T), torch.int32, dev)
     ql = None if q_len is None else _tensor("q_len", q_len, (B,), torch.int32, dev)
     with _On(dev, stream) as s:
-        st = _status(dev)
+        st = _status(parents)
         mask = torch.empty(B, T, (T + 63) // 64, dtype=torch.int64, device=dev)
         _check(lib().bsa_tree_mask(B, T, p, ql, mask.data_ptr(), st.data_ptr(), s))
     return mask, st
@@ -283,18 +309,16 @@ def _attend(name, q, cache, extra, q_len, layer, scale, out, lse, stream):
         _tensor("lse", lse, q.shape[:3], torch.float32, cache.device)
     shape = cache.shape()
     with _On(cache.device, stream) as s:
-        st = _status(cache.device)
+        st = _status(cache.refs)
         # rows past q_len are not written: 0 and -inf in tensors made here
         if out is None:
             out = torch.empty_like(q) if q_len is None else torch.zeros_like(q)
         if lse is None:
             lse = torch.full(q.shape[:3], float("-inf"), dtype=torch.float32, device=q.device) \
                 if q_len is not None else torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-        nb = lib().bsa_attend_paged_workspace_bytes(ctypes.byref(shape), cache.slots, cache.max_pages, Hq, T)
-        if nb == 0:
-            _bad(lib().bsa_last_error().decode(), BSA_ERR_UNSUPPORTED)
-        ws = _empty_bytes(nb, cache.device)
-        _check(getattr(lib(), name)(ctypes.byref(shape), cache.slots, cache.max_pages, Hq, T, qp, k, v,
+        nb = cache.workspace_bytes("attend_paged", Hq, T)
+        ws = cache._scratch(nb)
+        _check(getattr(lib(), name)(shape, cache.slots, cache.max_pages, Hq, T, qp, k, v,
                                     cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql, *extra, scale,
                                     out.data_ptr(), lse.data_ptr(), st.data_ptr(), ws.data_ptr(), nb, s))
     return out, lse, st
@@ -341,18 +365,16 @@ def select_pages(q: torch.Tensor, cache: PagedCache, cfg: PageSelectConfig, *, q
     params = PageSelectParams(cfg.k, cfg.n_first, cfg.n_last)
     dev = cache.device
     with _On(dev, stream) as s:
-        nb = lib().bsa_select_pages_workspace_bytes(ctypes.byref(shape), cache.slots, cache.max_pages, Hq, T)
-        if nb == 0:
-            _bad(lib().bsa_last_error().decode(), BSA_ERR_UNSUPPORTED)
+        nb = cache.workspace_bytes("select_pages", Hq, T)
         if not 1 <= cfg.k <= cache.max_pages:
             _bad("k must be 1..max_pages")
-        r = dict(kv_idx=torch.empty(cache.slots, H, T, cfg.k, dtype=torch.int32, device=dev),
-                 kv_cnt=torch.empty(cache.slots, H, T, dtype=torch.int32, device=dev),
+        r = dict(kv_idx=cache.refs.new_empty(cache.slots, H, T, cfg.k),
+                 kv_cnt=cache.refs.new_empty(cache.slots, H, T),
                  scores=(torch.empty(cache.slots, H, T, cache.max_pages, dtype=torch.float32, device=dev)
                          if want_scores else None),
-                 dev_status=_status(dev))
-        ws = None if want_scores else _empty_bytes(nb, dev)
-        _check(lib().bsa_select_pages(ctypes.byref(shape), ctypes.byref(params), cache.slots, cache.max_pages,
+                 dev_status=_status(cache.refs))
+        ws = None if want_scores else cache._scratch(nb)
+        _check(lib().bsa_select_pages(shape, ctypes.byref(params), cache.slots, cache.max_pages,
                                       Hq, T, qp, b, cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
                                       r["kv_idx"].data_ptr(), r["kv_cnt"].data_ptr(),
                                       r["scores"].data_ptr() if want_scores else None,
