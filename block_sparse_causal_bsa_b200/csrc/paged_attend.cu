@@ -9,11 +9,8 @@
 // TMA-fed stages that never drains between items, and the MMAs, exponentials and shared-memory
 // reads of a tile are spread over eight warps so that they stay under the time its bytes take.
 //
-// 288 threads:
-//   warp 0     producer: page numbers of the coming tiles in its lanes' registers (one table read
-//              per 8 to 32 tiles), then per tile one TMA box per page and 64-column half, lanes in
-//              parallel. Pages without a visible row are not read. Per stage it leaves the mask of
-//              the tile's rows that are keys of the item.
+// 320 threads:
+//   warps 0, 9 producers of K and of V (paged_feed.cuh)
 //   warps 1-8  two groups of four, taking tiles in turn; a warp owns 16 keys of its tiles and keeps its
 //              own online softmax over them (maximum m, sum l, unnormalised O):
 //                S = K Q^T (A = K rows by ldmatrix, B = Q in registers), P = 2^(S scale log2 e - m),
@@ -26,20 +23,18 @@
 // Rows that are no keys (the tail of the last page, missing pages) have their S masked and their
 // V rows zeroed in shared memory, and non-finite values of drafted tokens are taken out of the
 // tile and given back only to rows that see them.
-#include <limits.h>
 #include <math.h>
 
 #include <atomic>
 
-#include "paged_work.cuh"
-#include "tc_common.cuh"
+#include "paged_feed.cuh"
 
 namespace bsa {
 
 namespace {
 
 constexpr int kWarps = 8;                       // compute warps
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kThreads = 32 * (kWarps + 2);
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -108,7 +103,7 @@ struct __align__(16) Ctrl {
 template <int D, int RT>
 constexpr size_t smem_bytes() { return 1024 + Cfg<D, RT>::kStages * Cfg<D, RT>::kStage + sizeof(Ctrl<D, RT>); }
 
-// Four values of a row, final: normalised, with the non-finite drafted values, rounded and stored.
+// Four values of a row, final: normalised, rounded and stored, then the non-finite drafted values.
 template <int D, bool F16, bool LIST>
 __device__ __forceinline__ void store_row4(const PagedArgs& a, const Item& it, int r, int d4, float4 v, float mx,
                                            float ls, bool fixup) {
@@ -117,12 +112,9 @@ __device__ __forceinline__ void store_row4(const PagedArgs& a, const Item& it, i
   row_of<LIST>(a, it, r, head, t);
   const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
   const float inv = ls == 0.f ? 0.f : 1.f / ls;
-  float y[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-  if (!LIST && fixup) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) y[u] += nonfinite_drafts<F16>(a, it, t, d4 + u);
-  }
-  *reinterpret_cast<uint2*>(a.out + row * D + d4) = make_uint2(pack_16<F16>(y[0], y[1]), pack_16<F16>(y[2], y[3]));
+  *reinterpret_cast<uint2*>(a.out + row * D + d4) =
+      make_uint2(pack_16<F16>(v.x * inv, v.y * inv), pack_16<F16>(v.z * inv, v.w * inv));
+  if (!LIST && fixup) store_nonfinite<F16>(a, it, t, row, d4, d4 + 4);
   if (d4 == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
 }
 
@@ -139,21 +131,26 @@ template <int D, int RT, bool F16, bool LIST>
 __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const Parts<LIST, RT>& parts,
                                        Ctrl<D, RT>& c, int tid, bool ok) {
   constexpr int kU = 8;                          // reads in flight
-  const int np = parts.n;
+  // (copies: behind the ordered reads below, what the references name would be read again each time)
+  const float* const part_o = a.part_o;
+  const float2* const part_ml = reinterpret_cast<const float2*>(a.part_ml);
+  const int32_t* const part_flag = a.part_flag;
+  const Parts<LIST, RT> pt = parts;
+  const int np = pt.n, rows = it.rows;
   static_assert(sizeof(c.ml) >= kMaxPartsCtas * RT * sizeof(float2), "room for every part");
   for (int i = tid; i < np * RT; i += 32 * kWarps)
-    c.ml[i] = read_l2(reinterpret_cast<const float2*>(a.part_ml + (parts.slot(i / RT) * RT + i % RT) * 2));
+    c.ml[i] = read_l2(part_ml + pt.slot(i / RT) * RT + i % RT);
   if (!LIST)
     for (int i = tid; i < np; i += 32 * kWarps)
-      if (read_l2(a.part_flag + parts.slot(i))) atomicOr(&c.last, 2);
+      if (read_l2(part_flag + pt.slot(i))) atomicOr(&c.last, 2);
   float4 v[kU];
   auto read = [&](int i, int p0) {
     const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p0 + u < np && r < it.rows)
-        v[u] = read_l2(reinterpret_cast<const float4*>(a.part_o + (parts.slot(p0 + u) * RT + r) * D + d4));
+      if (p0 + u < np && r < rows)
+        v[u] = read_l2(reinterpret_cast<const float4*>(part_o + (pt.slot(p0 + u) * RT + r) * D + d4));
     }
   };
   if (tid < RT * (D / 4)) read(tid, 0);
@@ -197,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      tc::mbar_init(&c.full[s], 1);
+      tc::mbar_init(&c.full[s], 2);             // both producers
       tc::mbar_init(&c.empty[s], kWarps / 2);
     }
     c.abort_flag = 0;
@@ -211,97 +208,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
   Walk<LIST, RT> w;
   w.init(a);
   const long long x0 = w.start(blockIdx.x), x1 = w.start(blockIdx.x + 1);
-  int tiles_issued = 0;
+  int issued = 0;
 
-  if (warp == 0) {
-    // ---------------- producer ----------------
-    if (lane == 0) {
-      tc::prefetch_tmap(&tmk);
-      tc::prefetch_tmap(&tmv);
-    }
-    const int page = a.g.page, rpb = page < kTileKeys ? page : kTileKeys, npt = kTileKeys / rpb;
-    int n = 0;                                  // tiles so far
-    bool ok = true;
-    Item it;
-    if (x0 < x1) w.locate(a, x0, it);
-    for (long long x = x0; ok && x < x1;) {
-      const long long xe = min(x1, it.first + it.n_tiles);
-      int cnt;
-      bool bad;
-      const int live = item_live_tiles<LIST>(a, it, cnt, bad);
-      const int ta = (int)(x - it.first), tb = min((int)(xe - it.first), live);
-      const int32_t* table = a.g.table + (size_t)it.b * a.g.max_pages;
-      const int32_t* list = LIST ? a.kv_idx + (((size_t)it.b * a.g.Hkv + it.h) * a.g.T + it.t) * a.W : nullptr;
-      // positions below it are keys
-      const int limit = LIST ? (it.t < it.ql ? it.base + it.t + 1 : 0) : it.base + it.ql;
-      // Lane i: box (i % npt) of tile t0 + i / npt. The table entries of the batch after this one and
-      // the list entries of the one after that are on their way while a batch is issued.
-      const int per_load = 32 / npt;
-      auto entry = [&](int t0) -> int {          // the box's page number within the sequence, -1: none
-        const int tile = t0 + lane / npt;
-        if (!LIST && tile >= tb) return -1;
-        const int e = (tile * kTileKeys + (lane % npt) * rpb) / page;
-        if (!LIST) return e * page < limit ? e : -1;
-        if (e >= a.W) return INT_MIN;
-        const int j = __ldg(list + e);           // (within the row of W entries; not behind the count's read)
-        return e < cnt ? max(j, -1) : INT_MIN;
-      };
-      auto held = [&](int j) -> int {            // its page of the pool
-        return j >= 0 && (long long)j * page < limit ? __ldg(table + j) : -1;
-      };
-      int j_now = entry(ta), pg_now = held(j_now), j_next = entry(ta + per_load);
-      for (int t0 = ta; ok && t0 < tb; t0 += per_load) {
-        const int pg_next = held(j_next), j_next2 = entry(t0 + 2 * per_load);
-        const int off = ((t0 + lane / npt) * kTileKeys + (lane % npt) * rpb) % page;
-        int rows = 0, y = 0;
-        if (LIST ? j_now != INT_MIN && t0 + lane / npt < tb : j_now >= 0) {
-          if (j_now < 0 || (long long)j_now * page >= limit) {
-            bad = true;                          // a list entry past the token's page
-          } else {
-            rows = min(max(limit - (j_now * page + off), 0), rpb);
-            if (rows > 0 && (pg_now < 0 || pg_now >= a.g.n_pages)) {
-              bad = true;
-              rows = 0;
-            }
-            y = (int)(((long long)pg_now * a.g.Hkv + it.h) * page) + off;
-          }
-        }
-        unsigned long long bits = rows == 0 ? 0 : (rows == 64 ? ~0ull : (1ull << rows) - 1) << ((lane % npt) * rpb);
-        const int n_here = min(per_load, tb - t0);
-        for (int i = 0; i < n_here; ++i) {
-          const int s = n % C::kStages;
-          if (n >= C::kStages) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&c.empty[s], ((n / C::kStages) - 1) & 1, abort_flag, &c.status));
-            if (!ok) break;
-          }
-          const bool mine = lane / npt == i;
-          const unsigned boxes = __ballot_sync(0xffffffffu, mine && rows > 0);
-          const unsigned lo = __reduce_or_sync(0xffffffffu, mine ? (unsigned)bits : 0u);
-          const unsigned hi = __reduce_or_sync(0xffffffffu, mine ? (unsigned)(bits >> 32) : 0u);
-          if (lane == 0) {
-            c.vmask[s] = ((unsigned long long)hi << 32) | lo;
-            tc::mbar_arrive_expect_tx(&c.full[s], (uint32_t)(__popc(boxes) * rpb) * 2u * D * 2u);
-          }
-          __syncwarp();
-          if (mine && rows > 0) {
-            uint8_t* kd = sm + s * C::kStage + (lane % npt) * rpb * 128;
-#pragma unroll
-            for (int hh = 0; hh < C::kHalves; ++hh) {
-              tc::tma_load_2d(kd + hh * C::kHalf, &tmk, hh * 64, y, &c.full[s]);
-              tc::tma_load_2d(kd + C::kTile + hh * C::kHalf, &tmv, hh * 64, y, &c.full[s]);
-            }
-          }
-          ++n;
-        }
-        j_now = j_next;
-        pg_now = pg_next;
-        j_next = j_next2;
-      }
-      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&c.status, BSA_DEV_BAD_INDEX);
-      x = xe;
-      if (x < x1) w.next(a, it);
-    }
-    tiles_issued = n;
+  if (warp == 0 || warp == kWarps + 1) {
+    // ---------------- producers: K, V ----------------
+    const bool is_k = warp == 0;
+    const Feed<D> f{is_k ? &tmk : &tmv, sm + (is_k ? 0 : C::kTile), C::kStage, c.full, c.empty,
+                    is_k ? c.vmask : nullptr};
+    issued = feed_share<LIST, RT, D, C::kStages, C::kStages>(a, w, x0, x1, f, abort_flag, &c.status);
   } else {
     // ---------------- compute ----------------
     const int cw = warp - 1, group = cw / 4, kw = cw % 4;
@@ -547,9 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
 
   // ---------------- teardown ----------------
   __syncthreads();
+  if (issued > 0 && lane == 0) feed_drain<C::kStages>(c.full, issued);
   if (threadIdx.x == 0) {
-    for (int t = max(0, tiles_issued - C::kStages); t < tiles_issued; ++t)
-      tc::mbar_wait_timed(&c.full[t % C::kStages], (t / C::kStages) & 1);
     wait_prepared();                             // in every CTA: this kernel's end is that one's, too
     if (c.status) atomicOr(a.dev_status, c.status);
   }

@@ -8,8 +8,7 @@
 // per row and key, 16 a clock and SM) are never far behind. So every K and V tile is read once for up to
 // 256 rows, and two independent chains of products and softmax share it. One CTA per SM, 384
 // threads, all 512 columns of TMEM, walking its share of all key tiles (paged_work.cuh):
-//   warp 0      producer: page numbers in its lanes' registers, then per tile one TMA box per page and
-//               64-column half, K and V in separate stages
+//   warps 0, 3  producers of K and of V (paged_feed.cuh), separate stages
 //   warps 1, 2  one thread each issues the products of group 0 and of group 1: S_j = Q K_j^T into one of
 //               two TMEM buffers, S of the group's next tile before the value product of this one,
 //               and O += P_j V_j with P read from TMEM
@@ -29,8 +28,7 @@
 // the softmax warps mend the V tile in shared memory before they release P.
 #include <math.h>
 
-#include "paged_work.cuh"
-#include "tc_common.cuh"
+#include "paged_feed.cuh"
 
 namespace bsa {
 
@@ -109,8 +107,8 @@ __device__ __forceinline__ uint64_t draft_window(const PagedArgs& a, int b, int 
 
 // Parts lie transposed, [D / 4][RT] of four floats: a warp's rows are then neighbours both when a
 // part is written (a thread per row) and when parts are joined.
-__device__ __forceinline__ float4* part4(const PagedArgs& a, size_t slot, int D, int d4, int r) {
-  return reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + d4) * RT + r;
+__device__ __forceinline__ float4* part4(float* part_o, size_t slot, int D, int d4, int r) {
+  return reinterpret_cast<float4*>(part_o) + (slot * (D / 4) + d4) * RT + r;
 }
 // Joins the parts of the rows [r0, r0 + rows) of an item, channels 4 d0 .. 4 d1, one group: 128 / R
 // threads per row, R the rows rounded up to whole warps, each a run of channels; sixteen reads of 16
@@ -120,19 +118,24 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
                                        int rows, int d0, int d1, int flag_at, int tid, bool ok) {
   constexpr float kShift = F16 ? 7.f : 0.f;
   constexpr int kU = 8;
-  const int np = parts.n, R = (rows + 31) / 32 * 32;
+  // (copies: behind the ordered reads below, what the references name would be read again each time)
+  float* const part_o = a.part_o;
+  const float2* const part_ml = reinterpret_cast<const float2*>(a.part_ml);
+  const int32_t* const part_flag = a.part_flag;
+  const Parts<false, RT> pt = parts;
+  const int np = pt.n, R = (rows + 31) / 32 * 32;
   const int groups = 128 / R, dg = tid / R;                    // (R = 96: one group, 32 threads idle)
   if (dg >= groups || tid % R >= rows) return;
   const int r = r0 + tid % R;
   const int per = (d1 - d0 + groups - 1) / groups;
   const int da = d0 + dg * per, db = min(da + per, d1);
-  auto ml_of = [&](int i) { return reinterpret_cast<const float2*>(a.part_ml + (parts.slot(i) * RT + r) * 2); };
+  auto ml_of = [&](int i) { return part_ml + pt.slot(i) * RT + r; };
   float mx = -INFINITY, ls = 0.f;
   int flag = 0;
 #pragma unroll 4
   for (int i = 0; i < np; ++i) {
     mx = fmaxf(mx, read_l2(ml_of(i)).x);
-    flag |= read_l2(a.part_flag + 2 * parts.slot(i) + flag_at);
+    flag |= read_l2(part_flag + 2 * pt.slot(i) + flag_at);
   }
   int head, t;
   row_of<false>(a, it, r, head, t);
@@ -144,14 +147,14 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
     ls = 0.f;
     for (int i = 0; i < np; i += 2) {
       const int i1 = min(i + 1, np - 1);                       // (the odd last part counts once)
-      const size_t s0 = parts.slot(i), s1 = parts.slot(i1);
+      const size_t s0 = pt.slot(i), s1 = pt.slot(i1);
       const float2 m0 = read_l2(ml_of(i)), m1 = read_l2(ml_of(i1));
       float4 v[kU], w[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int d4 = min(dc + u, db - 1);
-        v[u] = read_l2(part4(a, s0, D, d4, r));
-        w[u] = read_l2(part4(a, s1, D, d4, r));
+        v[u] = read_l2(part4(part_o, s0, D, d4, r));
+        w[u] = read_l2(part4(part_o, s1, D, d4, r));
       }
       const float f = m0.x == -INFINITY ? 0.f : ex2(m0.x - mx);
       const float h = m1.x == -INFINITY || i1 == i ? 0.f : ex2(m1.x - mx);
@@ -178,16 +181,12 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
     for (int u = 0; u < kU; ++u) {
       const int d4 = dc + u;
       if (d4 >= db) break;
-      float y[4] = {acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv};
-      if (flag) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] += nonfinite_drafts<F16>(a, it, t, 4 * d4 + e);
-      }
       if (ok)
         *reinterpret_cast<uint2*>(a.out + row * D + 4 * d4) =
-            make_uint2(pack_16<F16>(y[0], y[1]), pack_16<F16>(y[2], y[3]));
+            make_uint2(pack_16<F16>(acc[u].x * inv, acc[u].y * inv), pack_16<F16>(acc[u].z * inv, acc[u].w * inv));
     }
   }
+  if (flag && ok) store_nonfinite<F16>(a, it, t, row, 4 * da, 4 * db);
   if (ok && da == 0 && a.lse) a.lse[row] = ls == 0.f ? -INFINITY : (mx - kShift + log2f(ls)) * 0.69314718055994531f;
 }
 
@@ -244,79 +243,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
   const long long x0 = w.start(blockIdx.x), x1 = w.start(blockIdx.x + 1);
   Item it;
   if (x0 < x1) w.locate(a, x0, it);
-  int k_issued = 0, v_issued = 0;
+  int issued = 0;
   bool mma_issued = false;
 
-  if (warp == 0) {
-    // ---------------- producer ----------------
-    if (lane == 0) {
-      tc::prefetch_tmap(&tmk);
-      tc::prefetch_tmap(&tmv);
-    }
-    const int page = a.g.page, rpb = page < kTileKeys ? page : kTileKeys, npt = kTileKeys / rpb;
-    const int per_load = 32 / npt;
-    int n = 0;
-    bool ok = true;
-    for (long long x = x0; ok && x < x1;) {
-      const long long xe = min(x1, it.first + it.n_tiles);
-      const int ta = (int)(x - it.first), tb = (int)(xe - it.first);
-      const int32_t* table = a.g.table + (size_t)it.b * a.g.max_pages;
-      const int limit = it.base + it.ql;
-      bool bad = false;
-      for (int t0 = ta; ok && t0 < tb; t0 += per_load) {
-        // lane i: box (i % npt) of tile t0 + i / npt
-        const int tile = t0 + lane / npt;
-        const int pos = tile * kTileKeys + (lane % npt) * rpb;
-        int rows = tile < tb ? min(max(limit - pos, 0), rpb) : 0, y = 0;
-        if (rows > 0) {
-          const int pg = table[pos / page];
-          if (pg < 0 || pg >= a.g.n_pages) {
-            bad = true;
-            rows = 0;
-          }
-          y = (int)(((long long)pg * a.g.Hkv + it.h) * page) + pos % page;
-        }
-        const unsigned long long bits =
-            rows == 0 ? 0 : (rows == 64 ? ~0ull : (1ull << rows) - 1) << ((lane % npt) * rpb);
-        const int n_here = min(per_load, tb - t0);
-        for (int i = 0; i < n_here; ++i) {
-          const int s = n % NS;
-          const bool mine = lane / npt == i;
-          const unsigned boxes = __ballot_sync(0xffffffffu, mine && rows > 0);
-          const unsigned lo = __reduce_or_sync(0xffffffffu, mine ? (unsigned)bits : 0u);
-          const unsigned hi = __reduce_or_sync(0xffffffffu, mine ? (unsigned)(bits >> 32) : 0u);
-          const uint32_t bytes = (uint32_t)(__popc(boxes) * rpb) * D * 2u;
-          const uint32_t row_off = (uint32_t)((lane % npt) * rpb) * 128u;
-          if (n >= NS) ok = warp_all(tc::mbar_wait(&c.k_empty[s], ((n / NS) - 1) & 1, abort_flag, status));
-          if (!ok) break;
-          if (lane == 0) {
-            c.vmask[n % kMaskRing] = ((unsigned long long)hi << 32) | lo;
-            tc::mbar_arrive_expect_tx(&c.k_full[s], bytes);
-          }
-          __syncwarp();
-          if (mine && rows > 0) {
-#pragma unroll
-            for (int hh = 0; hh < C::kHalves; ++hh)
-              tc::tma_load_2d(sm + C::kK + s * C::kTile + hh * C::kHalf + row_off, &tmk, hh * 64, y, &c.k_full[s]);
-          }
-          k_issued = n + 1;
-          if (n >= NS) ok = warp_all(tc::mbar_wait(&c.v_empty[s], ((n / NS) - 1) & 1, abort_flag, status));
-          if (!ok) break;
-          if (lane == 0) tc::mbar_arrive_expect_tx(&c.v_full[s], bytes);
-          __syncwarp();
-          if (mine && rows > 0) {
-#pragma unroll
-            for (int hh = 0; hh < C::kHalves; ++hh)
-              tc::tma_load_2d(sm + C::kV + s * C::kTile + hh * C::kHalf + row_off, &tmv, hh * 64, y, &c.v_full[s]);
-          }
-          v_issued = n + 1;
-          ++n;
-        }
-      }
-      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(status, BSA_DEV_BAD_INDEX);
-      x = xe;
-      if (x < x1) w.next(a, it);
-    }
+  if (warp == 0 || warp == 3) {
+    // ---------------- producers: K, V ----------------
+    const bool is_k = warp == 0;
+    const Feed<D> f{is_k ? &tmk : &tmv, sm + (is_k ? C::kK : C::kV), C::kTile, is_k ? c.k_full : c.v_full,
+                    is_k ? c.k_empty : c.v_empty, is_k ? c.vmask : nullptr};
+    issued = feed_share<false, RT, D, NS, kMaskRing>(a, w, x0, x1, f, abort_flag, status);
   } else if (warp <= 2) {
     // ---------------- MMA issuers ----------------
     // (the walk is the whole warp's; one lane waits and issues)
@@ -450,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
           const int row = tid / 2;
           const bool key = (vm >> row) & 1;
           if (!key || (drafts && pos0 + row >= it.base)) {
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < D / 16; ++i) {
               const int ch = (tid & 1) * (D / 16) + i;
               uint4* p = reinterpret_cast<uint4*>(sm + C::kV + (n % NS) * C::kTile + (ch >> 3) * C::kHalf + row * 128 +
@@ -583,10 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
       const int fixup = *(volatile int*)&c.flag[g][seg & 1];
       if (ok && live) {
         const float inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-#pragma unroll
-        for (int ci = 0; ci < kCh; ++ci) {
-          if (ci >= c1 - c0) break;
-          const int cc = c0 + ci;
+#pragma unroll 1
+        for (int cc = c0; cc < c1; ++cc) {
           uint32_t v[32];
           __syncwarp();
           tc::tmem_ld32(tl + cc * 32, v);
@@ -601,21 +534,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
           }
           if (row_ok && whole) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              if (fixup) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[i + e] += nonfinite_drafts<F16>(a, it, t, cc * 32 + i + e);
-              }
+            for (int i = 0; i < 32; i += 8)
               *reinterpret_cast<uint4*>(a.out + grow * D + cc * 32 + i) =
                   make_uint4(pack_16<F16>(y[i], y[i + 1]), pack_16<F16>(y[i + 2], y[i + 3]),
                              pack_16<F16>(y[i + 4], y[i + 5]), pack_16<F16>(y[i + 6], y[i + 7]));
-            }
           } else if (row_ok) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              *part4(a, slot, D, cc * 8 + i, r) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+              *part4(a.part_o, slot, D, cc * 8 + i, r) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
           }
         }
+        if (fixup && whole && row_ok) store_nonfinite<F16>(a, it, t, grow, c0 * 32, c1 * 32);
         if (row_ok && c0 == 0) {
           if (whole) {
             if (a.lse) a.lse[grow] = l == 0.f ? -INFINITY : (m_used - kShift + log2f(l)) * 0.69314718055994531f;
@@ -647,9 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
   // ---------------- teardown ----------------
   tc::tc_fence_before();
   __syncthreads();
+  if (issued > 0 && lane == 0) feed_drain<NS>(warp == 0 ? c.k_full : c.v_full, issued);
   if (threadIdx.x == 0) {
-    for (int j = max(0, k_issued - NS); j < k_issued; ++j) tc::mbar_wait_timed(&c.k_full[j % NS], (j / NS) & 1);
-    for (int j = max(0, v_issued - NS); j < v_issued; ++j) tc::mbar_wait_timed(&c.v_full[j % NS], (j / NS) & 1);
     wait_prepared();                             // in every CTA: this kernel's end is that one's, too
     if (c.status) atomicOr(a.dev_status, c.status);
   }

@@ -85,7 +85,7 @@ struct Walk {
     return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
   }
   // slot b0 + lane
-  __device__ void load(const PagedArgs& a, int b0) {
+  __device__ static void load(const PagedArgs& a, int b0, long long& tiles, int& base, int& ql) {
     const int b = b0 + threadIdx.x % 32;
     base = ql = 0;
     if (b < a.g.slots) query_span(a.g, b, base, ql);
@@ -99,7 +99,7 @@ struct Walk {
     } else {
       long long s = 0;
       for (int b0 = (a.g.slots - 1) / 32 * 32; b0 >= 0; b0 -= 32) {    // (the first slots stay loaded)
-        load(a, b0);
+        load(a, b0, tiles, base, ql);
         s += tiles;
       }
 #pragma unroll
@@ -135,16 +135,18 @@ struct Walk {
   }
 
   // The item of tile x (0 <= x < total). Whole warp.
-  __device__ void locate(const PagedArgs& a, long long x, Item& it) {
+  __device__ void locate(const PagedArgs& a, long long x, Item& it) const {
     if (LIST) {
       set_list_item(a, divide(x, list_tiles(a)), it);
       return;
     }
     const int lane = threadIdx.x % 32;
     long long before = 0;
+    long long lt = tiles;                           // (locals: the members stay the first slots')
+    int lb = base, lq = ql;
     for (int b0 = 0; b0 < a.g.slots; b0 += 32) {
-      if (b0) load(a, b0);
-      long long p = tiles;                          // inclusive prefix
+      if (b0) load(a, b0, lt, lb, lq);
+      long long p = lt;                             // inclusive prefix
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, p, o);
@@ -153,10 +155,10 @@ struct Walk {
       const unsigned m = __ballot_sync(0xffffffffu, before + p > x);
       if (m) {
         const int l = __ffs(m) - 1;
-        const long long first = before + __shfl_sync(0xffffffffu, p - tiles, l);
+        const long long first = before + __shfl_sync(0xffffffffu, p - lt, l);
         it.b = b0 + l;
-        it.base = __shfl_sync(0xffffffffu, base, l);
-        it.ql = __shfl_sync(0xffffffffu, ql, l);
+        it.base = __shfl_sync(0xffffffffu, lb, l);
+        it.ql = __shfl_sync(0xffffffffu, lq, l);
         set_slot_item(a, first, (int)divide(x - first, ceil_div_i(it.base + it.ql, kTileKeys)), it);
         return;
       }
@@ -254,22 +256,25 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
   return lo || hi;
 }
 
-// The sum of the non-finite drafted values of channel d that token t sees: the kernels take such
-// values as zero (a weight of zero times NaN or infinity would reach rows that do not see them)
-// and the rows that do see them get them here.
+// The kernels take non-finite values of drafted tokens as zero (a weight of zero times NaN or infinity
+// would reach rows that do not see them). Where a tile had some, the rows that do see them get them
+// here, after their result is stored: channels [d0, d1) of output row `row` (token t), whose sum of such
+// values is NaN or infinite, get it added.
 template <bool F16>
-__device__ __noinline__ float nonfinite_drafts(const PagedArgs& a, const Item& it, int t, int d) {
-  float s = 0.f;
-  for (int j = 0; j < it.ql; ++j) {
-    if (!sees_draft(a, it.b, t, j)) continue;
-    const int pos = it.base + j;
-    const int pg = a.g.table[(size_t)it.b * a.g.max_pages + pos / a.g.page];
-    if (pg < 0 || pg >= a.g.n_pages) continue;
-    const float x = cvt_f32<F16>(
-        a.v[(((size_t)pg * a.g.Hkv + it.h) * a.g.page + pos % a.g.page) * a.g.d + d]);
-    if (!isfinite(x)) s += x;
+__device__ __noinline__ void store_nonfinite(const PagedArgs& a, const Item& it, int t, size_t row, int d0, int d1) {
+  for (int d = d0; d < d1; ++d) {
+    float s = 0.f;
+    for (int j = 0; j < it.ql; ++j) {
+      if (!sees_draft(a, it.b, t, j)) continue;
+      const int pos = it.base + j;
+      const int pg = a.g.table[(size_t)it.b * a.g.max_pages + pos / a.g.page];
+      if (pg < 0 || pg >= a.g.n_pages) continue;
+      const float x = cvt_f32<F16>(a.v[(((size_t)pg * a.g.Hkv + it.h) * a.g.page + pos % a.g.page) * a.g.d + d]);
+      if (!isfinite(x)) s += x;
+    }
+    uint16_t* o = a.out + row * a.g.d + d;
+    if (!isfinite(s)) *o = cvt_16<F16>(cvt_f32<F16>(*o) + s);
   }
-  return s;
 }
 
 // Reads from L2 of what other SMs wrote in this kernel. (volatile: they stay behind the barrier or
