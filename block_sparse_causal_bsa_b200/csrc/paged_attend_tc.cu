@@ -48,7 +48,7 @@ struct Cfg {
   static constexpr uint32_t kQTile = kHalves * kQHalf;
   static constexpr uint32_t kHalf = kTileKeys * 128;
   static constexpr uint32_t kTile = kHalves * kHalf;
-  static constexpr int NS = D == 128 ? 5 : 8;
+  static constexpr int NS = D == 128 ? 4 : 8;     // even: a stage's tiles are one group's where they take turns
   static constexpr size_t kQ = 0, kK = 2 * kQTile, kV = kK + NS * kTile, kCtrl = kV + NS * kTile;
 };
 constexpr int kMaxStages = 8;
@@ -203,13 +203,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl& c = *reinterpret_cast<Ctrl*>(sm + C::kCtrl);
   const uint32_t sQ = tc::smem_u32(sm + C::kQ), sK = tc::smem_u32(sm + C::kK), sV = tc::smem_u32(sm + C::kV);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       tc::mbar_init(&c.k_full[s], 1);
       tc::mbar_init(&c.v_full[s], 1);
-      tc::mbar_init(&c.k_empty[s], 2);          // both issuers
+      tc::mbar_init(&c.k_empty[s], 2);          // both issuers, or twice the one whose tile it was
       tc::mbar_init(&c.v_empty[s], 2);
     }
     for (int g = 0; g < 2; ++g) {
@@ -254,83 +254,85 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
     issued = feed_share<false, RT, D, NS, kMaskRing>(a, w, x0, x1, f, abort_flag, status);
   } else if (warp <= 2) {
     // ---------------- MMA issuers ----------------
-    // (the walk is the whole warp's; one lane waits and issues)
+    // The whole warp walks, waits and computes descriptors, one elected lane issues: with the products
+    // inside a branch of one lane their operands would have to be moved to uniform registers one by one.
     constexpr uint32_t idS = F16 ? tc::idesc_f16_f32(128, 64, false, false) : tc::idesc_bf16_f32(128, 64, false, false);
     constexpr uint32_t idPV = F16 ? tc::idesc_f16_f32(128, D, false, true) : tc::idesc_bf16_f32(128, D, false, true);
     const int g = warp - 1;
     Group& b = c.g[g];
-    const uint32_t sQg = sQ + g * C::kQTile, tg = tmem + g * 256;
+    const uint32_t tg = tmem + g * 256;
+    const uint64_t descQ = tc::sdesc_sw128(sQ + g * C::kQTile, 16, 1024);
+    const uint64_t descK = tc::sdesc_sw128(sK, 16, 1024), descV = tc::sdesc_sw128(sV, C::kHalf, 1024);
     int n = 0, seg = 0, js = 0, jv = 0;          // tiles of the CTA; products of this group issued
     bool ok = true;
-    for (long long x = x0; x < x1; ++seg) {
+    for (long long x = x0; ok && x < x1; ++seg) {
       const long long xe = min(x1, it.first + it.n_tiles);
       const int L = (int)(xe - x);
-      if (lane == 0 && ok) {
-        const bool share = it.rows <= GR;        // the groups take the tiles in turn
-        int si = 0;                              // next tile of the segment to be looked at for S
-        const int js0 = js;
-        // S of the group's next tile; the tiles of the other group on the way are released
-        auto next_s = [&]() {
-          for (bool mine = false; ok && !mine && si < L; ++si) {
-            const int s = (n + si) % NS;
-            ok = tc::mbar_wait(&c.k_full[s], ((n + si) / NS) & 1, abort_flag, status);
-            if (!ok) break;
-            mine = !share || ((n + si) & 1) == g;
-            if (!mine) {
-              tc::mbar_arrive(&c.k_empty[s]);
-              continue;
-            }
-            // S overwrites the buffer whose P the value product of two tiles ago read. (For the first of
-            // a segment every product has landed, as Q's arrival says; the parity of two ago would
-            // wait for the next one.)
-            if (js >= 2 && js > js0) ok = tc::mbar_wait(&b.o_ready, js & 1, abort_flag, status);
-            if (!ok) break;
-            tc::tc_fence_after();
-            const uint32_t kb = sK + s * C::kTile, d = tg + kColS + (js % 2) * 64;
+      const bool share = it.rows <= GR;          // the groups take the tiles in turn
+      const int step = share ? 2 : 1, i0 = share ? (n ^ g) & 1 : 0;
+      int si = i0;                               // the group's next tile of the segment to get its S
+      auto next_s = [&]() {
+        if (si >= L) return;
+        const int s = (n + si) % NS;
+        ok = tc::mbar_wait(&c.k_full[s], ((n + si) / NS) & 1, abort_flag, status);
+        // S overwrites the buffer whose P the value product of two tiles ago read. (For the first of
+        // a segment every product has landed, as Q's arrival says; the parity of two ago would
+        // wait for the next one.)
+        if (ok && js >= 2 && si != i0) ok = tc::mbar_wait(&b.o_ready, js & 1, abort_flag, status);
+        ok = warp_all(ok);
+        if (!ok) return;
+        tc::tc_fence_after();
+        const uint32_t d = tg + kColS + (js % 2) * 64;
+        const uint64_t kd = descK + (uint64_t)(s * (C::kTile >> 4));
+        if (tc::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t qoff = (kk >> 2) * C::kQHalf + (kk & 3) * 32;
-              const uint32_t koff = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-              tc::umma_bf16(d, tc::sdesc_sw128(sQg + qoff, 16, 1024), tc::sdesc_sw128(kb + koff, 16, 1024), idS, kk > 0);
-            }
-            tc::mbar_arrive(&b.s_full[js % 2]);
-            tc::umma_commit(&b.s_full[js % 2]);
-            tc::umma_commit(&c.k_empty[s]);
-            mma_issued = true;
-            ++js;
-          }
-        };
-        ok = tc::mbar_wait(&b.q_full, seg & 1, abort_flag, status);
-        if (ok) next_s();
-        bool first = true;
-        for (int i = 0; ok && i < L; ++i) {
-          const int s = (n + i) % NS;
-          if (share && ((n + i) & 1) != g) {
-            ok = tc::mbar_wait(&c.v_full[s], ((n + i) / NS) & 1, abort_flag, status);
-            if (ok) tc::mbar_arrive(&c.v_empty[s]);
-            continue;
-          }
-          next_s();
-          if (!ok) break;
-          ok = tc::mbar_wait(&c.v_full[s], ((n + i) / NS) & 1, abort_flag, status) &&
-               tc::mbar_wait(&b.p_full, jv & 1, abort_flag, status);
-          if (!ok) break;
-          tc::tc_fence_after();
-          const uint32_t vb = sV + s * C::kTile, pa = tg + kColS + (jv % 2) * 64;
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::umma_bf16(d, descQ + (((kk >> 2) * C::kQHalf + (kk & 3) * 32) >> 4),
+                          kd + (((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4), idS, kk > 0);
+          tc::mbar_arrive(&b.s_full[js % 2]);
+          tc::umma_commit(&b.s_full[js % 2]);
+          tc::umma_commit(&c.k_empty[s]);
+          if (share) tc::umma_commit(&c.k_empty[s]);
+        }
+        __syncwarp();
+        mma_issued = true;
+        ++js;
+        si += step;
+      };
+      ok = warp_all(tc::mbar_wait(&b.q_full, seg & 1, abort_flag, status));
+      if (ok) next_s();
+      uint32_t add = 0;
+      for (int i = i0; ok && i < L; i += step) {
+        const int s = (n + i) % NS;
+        next_s();
+        if (!ok) break;
+        ok = warp_all(tc::mbar_wait(&c.v_full[s], ((n + i) / NS) & 1, abort_flag, status) &&
+                      tc::mbar_wait(&b.p_full, jv & 1, abort_flag, status));
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint32_t pa = tg + kColS + (jv % 2) * 64;
+        const uint64_t vd = descV + (uint64_t)(s * (C::kTile >> 4));
+        if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc::umma_bf16_ts(tg, pa + kk * 8, tc::sdesc_sw128(vb + kk * 2048, C::kHalf, 1024), idPV,
-                             (!first || kk > 0) ? 1u : 0u);
+            tc::umma_bf16_ts(tg, pa + kk * 8, vd + kk * (2048 >> 4), idPV, kk > 0 ? 1u : add);
           tc::umma_commit(&b.o_ready);
           tc::umma_commit(&c.v_empty[s]);
-          first = false;
-          ++jv;
+          if (share) tc::umma_commit(&c.v_empty[s]);
         }
+        __syncwarp();
+        add = 1;
+        ++jv;
       }
-      __syncwarp();
       n += L;
       x = xe;
       if (x < x1) w.next(a, it);
+    }
+    // what the elected lane has in flight completes before the teardown
+    if (mma_issued) {
+      if (tc::elect_one()) tc::umma_commit(&b.done);
+      __syncwarp();
+      if (lane == 0) tc::mbar_wait_timed(&b.done, 0);
     }
   } else if (warp >= 4) {
     // ---------------- softmax warps ----------------
@@ -581,13 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
     wait_prepared();                             // in every CTA: this kernel's end is that one's, too
     if (c.status) atomicOr(a.dev_status, c.status);
   }
-  if ((warp == 1 || warp == 2) && lane == 0 && mma_issued) {
-    // every MMA this thread issued has completed once this commit arrives
-    tc::umma_commit(&c.g[warp - 1].done);
-    tc::mbar_wait_timed(&c.g[warp - 1].done, 0);
-  }
-  __syncthreads();
   if (warp == 3) {
+    __syncwarp();
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
