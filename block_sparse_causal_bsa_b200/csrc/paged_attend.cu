@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
     Item it;
     if (x0 < x1) w.locate(a, x0, it);
     for (long long x = x0; x < x1; ++seg) {
-      const long long xe = min(x1, it.first + it.n_tiles);
+      const long long xe = min(x1, it.first + it.units());
       int cnt;
       bool bad;
       const int live = item_live_tiles<LIST>(a, it, cnt, bad);

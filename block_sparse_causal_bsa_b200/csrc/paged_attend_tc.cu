@@ -68,6 +68,7 @@ struct __align__(16) Ctrl {
   int32_t status;
   int flag[2][2];                               // [group][segment parity]: non-finite drafts taken out
   int last[2];                                  // [group]: this CTA joins the item's parts
+  float2 ml[2][GR];                             // [group]: maxima and sums of shared segments
 };
 
 template <int D>
@@ -140,6 +141,7 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
   int head, t;
   row_of<false>(a, it, r, head, t);
   const size_t row = ((size_t)it.b * a.Hq + head) * a.g.T + t;
+  uint16_t* const out = a.out + row * D;
   for (int dc = da; dc < db; dc += kU) {
     float4 acc[kU];
 #pragma unroll
@@ -177,13 +179,15 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
       }
     }
     const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    // (runs are even: 16 bytes a store)
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int d4 = dc + u;
-      if (d4 >= db) break;
+    for (int u = 0; u < kU; u += 2) {
+      if (dc + u >= db) break;
       if (ok)
-        *reinterpret_cast<uint2*>(a.out + row * D + 4 * d4) =
-            make_uint2(pack_16<F16>(acc[u].x * inv, acc[u].y * inv), pack_16<F16>(acc[u].z * inv, acc[u].w * inv));
+        *reinterpret_cast<uint4*>(out + 4 * (dc + u)) =
+            make_uint4(pack_16<F16>(acc[u].x * inv, acc[u].y * inv), pack_16<F16>(acc[u].z * inv, acc[u].w * inv),
+                       pack_16<F16>(acc[u + 1].x * inv, acc[u + 1].y * inv),
+                       pack_16<F16>(acc[u + 1].z * inv, acc[u + 1].w * inv));
     }
   }
   if (flag && ok) store_nonfinite<F16>(a, it, t, row, 4 * da, 4 * db);
@@ -266,8 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
     int n = 0, seg = 0, js = 0, jv = 0;          // tiles of the CTA; products of this group issued
     bool ok = true;
     for (long long x = x0; ok && x < x1; ++seg) {
-      const long long xe = min(x1, it.first + it.n_tiles);
-      const int L = (int)(xe - x);
+      const long long xe = min(x1, it.first + it.units());
+      int ta, tb;
+      it.tiles_of(x, xe, ta, tb);
+      const int L = tb - ta;
       const bool share = it.rows <= GR;          // the groups take the tiles in turn
       const int step = share ? 2 : 1, i0 = share ? (n ^ g) & 1 : 0;
       int si = i0;                               // the group's next tile of the segment to get its S
@@ -343,32 +349,57 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
     const int rt = quarter * 32 + lane;                  // row of the group's tile
     const uint32_t tl = tmem + g * 256 + ((uint32_t)(quarter * 32) << 16);
     const float scale_log2 = a.scale_log2;
+    // This thread's row of an item: output row and token. r0, rows: the group's rows.
+    struct Row {
+      int r0, rows, t;
+      bool ok;
+      size_t row;
+    };
+    auto row_in = [&](const Item& i) {
+      Row o;
+      o.r0 = i.rows <= GR ? 0 : g * GR;
+      o.rows = min(GR, i.rows - o.r0);
+      o.ok = rt < o.rows;
+      int head;
+      row_of<false>(a, i, o.ok ? o.r0 + rt : 0, head, o.t);
+      o.row = ((size_t)i.b * a.Hq + head) * a.g.T + o.t;
+      return o;
+    };
+    // Q of an item: the copies start, and (later) have landed. No product that reads the previous Q is
+    // left when they start.
+    uint8_t* const qs = sm + C::kQ + g * C::kQTile + rt * 128;
+    auto load_q = [&](const Row& o) {
+      const uint4* qr = reinterpret_cast<const uint4*>(a.q + o.row * D);
+#pragma unroll
+      for (int ch = 0; ch < D / 8; ++ch) {
+        uint8_t* dst = qs + (ch >> 3) * C::kQHalf + (((ch & 7) ^ (rt & 7)) << 4);
+        if (o.ok) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(qr + ch) : "memory");
+        else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto q_landed = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&b.q_full);
+    };
     int n = 0, seg = 0, j = 0;                           // j: tiles of this group
     bool ok = true;
+    Row me{};
+    if (x0 < x1) {
+      me = row_in(it);
+      load_q(me);
+      q_landed();
+    }
     for (long long x = x0; x < x1; ++seg) {
-      const long long xe = min(x1, it.first + it.n_tiles);
-      const int ta = (int)(x - it.first), tb = (int)(xe - it.first);
+      const long long xe = min(x1, it.first + it.units());
+      int ta, tb;
+      it.tiles_of(x, xe, ta, tb);
       const bool share = it.rows <= GR;
-      const int r0 = share ? 0 : g * GR, rows = min(GR, it.rows - r0);     // the group's rows
-      const int r = r0 + rt;
-      const bool row_ok = rt < rows;
+      const int r0 = me.r0, rows = me.rows, t = me.t, r = r0 + rt;
+      const bool row_ok = me.ok;
       const bool live = quarter * 32 < rows;             // the warp has rows
-      int head, t;
-      row_of<false>(a, it, row_ok ? r : 0, head, t);
-      const size_t grow = ((size_t)it.b * a.Hq + head) * a.g.T + t;
-      {
-        // every product that read the previous Q has completed: its S was read below
-        const uint4* qr = reinterpret_cast<const uint4*>(a.q + grow * D);
-#pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch) {
-          const uint4 v = row_ok ? __ldg(qr + ch) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(sm + C::kQ + g * C::kQTile + (ch >> 3) * C::kQHalf + rt * 128 +
-                                    (((ch & 7) ^ (rt & 7)) << 4)) = v;
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&b.q_full);
-      }
+      const size_t grow = me.row;
       float m_used = -INFINITY, l = 0.f;
       bool first = true;                                 // no tile of the group in this segment yet
       for (int tile = ta; tile < tb; ++tile, ++n) {
@@ -483,8 +514,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
       // ---- result, or partial result ----
       if (ok && j > 0) ok = warp_all(tc::mbar_wait(&b.o_ready, (j - 1) & 1, abort_flag, status));
       tc::tc_fence_after();
-      const bool whole = ta == 0 && tb == it.n_tiles;
-      const size_t slot = 2 * (size_t)blockIdx.x + (ta == 0 ? 1 : 0);
+      // the next item's Q is on its way while this one's result is written
+      Item nx = it;
+      if (xe < x1) {
+        w.next(a, nx);
+        me = row_in(nx);
+        load_q(me);
+      }
+      const bool whole = x == it.first && xe == it.first + it.units();
+      const size_t slot = 2 * (size_t)blockIdx.x + (x == it.first ? 1 : 0);
       constexpr int kCh = D / 32;                        // pieces of 32 channels
       const int c0 = share ? g * (kCh / 2) : 0, c1 = share ? c0 + kCh / 2 : kCh;     // the group's
       auto tail_sync = [&]() {
@@ -492,15 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
         else group_sync(g);
       };
       float f0 = first ? 0.f : 1.f, f1 = 0.f;            // weights of the group's state and of the other's
-      if (share) {
-        // maximum and sum, over the S that was read
-        uint32_t v[16];
-        v[0] = __float_as_uint(m_used);
-        v[1] = __float_as_uint(l);
-#pragma unroll
-        for (int i = 2; i < 16; ++i) v[i] = 0u;
-        tc::tmem_st16(tl + kColS, v);
-      }
+      if (share) c.ml[g][rt] = make_float2(m_used, l);
       tc::tc_fence_before();
       // the flags and states are there (and no group is more than a segment ahead, whose flags are the
       // other pair's)
@@ -508,13 +538,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
       tc::tc_fence_after();
       const uint32_t other = tl - g * 256 + (1 - g) * 256;
       if (share) {
-        uint32_t v[16];
-        tc::tmem_ld16(other + kColS, v);
-        const float mo = __uint_as_float(v[0]);
-        const float m = fmaxf(m_used, mo);
+        const float2 o = c.ml[1 - g][rt];
+        const float m = fmaxf(m_used, o.x);
         f0 = m_used == -INFINITY ? 0.f : ex2(m_used - m);
-        f1 = mo == -INFINITY ? 0.f : ex2(mo - m);
-        l = l * f0 + __uint_as_float(v[1]) * f1;
+        f1 = o.x == -INFINITY ? 0.f : ex2(o.x - m);
+        l = l * f0 + o.y * f1;
         m_used = m;
       }
       const int fixup = *(volatile int*)&c.flag[g][seg & 1];
@@ -557,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
         __syncwarp();
         tc::tc_fence_before();
       }
+      if (xe < x1) q_landed();                           // S of its first tile may start
       if (!whole) {
         // ---- arrival; the last CTA joins the parts ----
         const int at = share ? 0 : g;
@@ -568,10 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
         tail_sync();
         if (c.last[at]) join_rows<D, F16>(a, it, parts, r0, rows, c0 * 8, c1 * 8, at, tid, ok);
       }
-      tail_sync();                                       // Q, the states and the flags may be written again
+      tail_sync();                                       // O, the states and the flags may be written again
       if (tid == 0) c.flag[g][seg & 1] = 0;              // next used two segments on, behind barriers
       x = xe;
-      if (x < x1) w.next(a, it);
+      it = nx;
     }
   }
 

@@ -41,12 +41,15 @@ __device__ __noinline__ int feed_share(const PagedArgs& a, Walk<LIST, RT> w, lon
   uint32_t parity = 1;
   bool bad = false;
   for (long long x = x0; x < x1;) {
-    const long long xe = min(x1, it.first + it.n_tiles);
+    const long long xe = min(x1, it.first + it.units());
     int cnt;
     bool bad_count;
     const int live = item_live_tiles<LIST>(a, it, cnt, bad_count);
     bad |= bad_count;
-    const int ta = (int)(x - it.first), tb = min((int)(xe - it.first), live), h = it.h;
+    int ta, tb;
+    it.tiles_of(x, xe, ta, tb);
+    tb = min(tb, live);
+    const int h = it.h;
     const int32_t* table = a.g.table + (size_t)it.b * a.g.max_pages;
     const int32_t* list = LIST ? a.kv_idx + (((size_t)it.b * Hkv + h) * a.g.T + it.t) * W : nullptr;
     // positions below it are keys

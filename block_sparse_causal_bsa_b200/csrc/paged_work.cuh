@@ -5,8 +5,9 @@
 //   whole cache  (slot, KV head, row tile): rows r of the G * ql (head of the group, token) pairs
 //                of the slot, RT at a time, r = g * ql + t
 //   page lists   (slot, KV head, token): the G heads of the group
-// Its keys come in tiles of 64. All items' tiles are laid end to end and every CTA takes an equal,
-// contiguous share of them, so ragged lengths balance without the host knowing them. A share may
+// Its keys come in tiles of 64. All items' tiles are laid end to end (those of row tiles of 256 with more
+// than 128 rows count twice: they take about twice as long) and every CTA takes an equal, contiguous
+// share of them, so ragged lengths balance without the host knowing them. A share may
 // begin or end inside an item: such segments leave a partial result (running maximum, sum,
 // unnormalised output) in one of the CTA's two slots of the workspace, 0 for a segment that starts
 // inside its item, 1 for one that starts with it. The CTA that arrives last at an item's counter joins its
@@ -55,7 +56,18 @@ struct Item {
   int row0, rows;                   // whole cache: first row and number of rows (<= RT)
   int t;                            // page lists: the token
   int n_tiles;                      // tiles of the item (page lists: of a full list)
-  long long first;                  // its first tile in the whole order
+  int weight;                       // what a tile counts in the whole order
+  long long first;                  // the item's first place there
+  __device__ int units() const { return n_tiles * weight; }
+  // Tiles of the places [x, xe) of the item: a tile belongs to the share that holds its first place.
+  __device__ void tiles_of(long long x, long long xe, int& ta, int& tb) const {
+    ta = (int)(x - first);
+    tb = (int)(xe - first);
+    if (weight == 2) {
+      ta = (ta + 1) / 2;
+      tb = (tb + 1) / 2;
+    }
+  }
 };
 
 // How far a share may shrink: below this many tiles per CTA the arrival and the join cost more time
@@ -65,8 +77,8 @@ constexpr int kMinTiles = RT == 256 ? 2 : 4;
 
 template <bool LIST, int RT>
 struct Walk {
-  long long total;                  // tiles of all items
-  long long per;                    // tiles per CTA (the last ones may have fewer, or none)
+  long long total;                  // weighted tiles of all items
+  long long per;                    // ... per CTA (the last ones may have fewer, or none)
   // lane b (whole cache): slot b's tiles and tokens
   long long tiles;
   int base, ql;
@@ -74,8 +86,9 @@ struct Walk {
   __device__ static int slot_items(const PagedArgs& a, int ql) {
     return a.g.Hkv * ceil_div_i(a.G * ql, RT);
   }
+  __device__ static int tile_weight(const PagedArgs& a, int ql) { return RT == 256 && a.G * ql > 128 ? 2 : 1; }
   __device__ static long long slot_tiles(const PagedArgs& a, int base, int ql) {
-    return ql ? (long long)slot_items(a, ql) * ceil_div_i(base + ql, kTileKeys) : 0;
+    return ql ? (long long)slot_items(a, ql) * ceil_div_i(base + ql, kTileKeys) * tile_weight(a, ql) : 0;
   }
   __device__ static int list_tiles(const PagedArgs& a) {
     return (int)(((long long)a.W * a.g.page + kTileKeys - 1) / kTileKeys);
@@ -114,6 +127,7 @@ struct Walk {
 
   __device__ void set_list_item(const PagedArgs& a, long long item, Item& it) const {
     it.n_tiles = list_tiles(a);
+    it.weight = 1;
     it.first = item * it.n_tiles;
     it.t = (int)item % a.g.T;                        // (slots * Hq * T is below 2^31)
     const int bh = (int)item / a.g.T;
@@ -126,7 +140,8 @@ struct Walk {
   // it.b, it.base and it.ql are set
   __device__ void set_slot_item(const PagedArgs& a, long long slot_first, int item, Item& it) const {
     it.n_tiles = ceil_div_i(it.base + it.ql, kTileKeys);
-    it.first = slot_first + (long long)item * it.n_tiles;
+    it.weight = tile_weight(a, it.ql);
+    it.first = slot_first + (long long)item * it.units();
     const int M = a.G * it.ql, mts = ceil_div_i(M, RT);
     it.h = mts == 1 ? item : item / mts;
     it.row0 = (item - it.h * mts) * RT;
@@ -159,7 +174,7 @@ struct Walk {
         it.b = b0 + l;
         it.base = __shfl_sync(0xffffffffu, lb, l);
         it.ql = __shfl_sync(0xffffffffu, lq, l);
-        set_slot_item(a, first, (int)divide(x - first, ceil_div_i(it.base + it.ql, kTileKeys)), it);
+        set_slot_item(a, first, (int)divide(x - first, ceil_div_i(it.base + it.ql, kTileKeys) * tile_weight(a, it.ql)), it);
         return;
       }
       before += __shfl_sync(0xffffffffu, p, 31);
@@ -167,7 +182,7 @@ struct Walk {
   }
   // The item after it (there is one: it ends before total).
   __device__ void next(const PagedArgs& a, Item& it) const {
-    const long long x = it.first + it.n_tiles;
+    const long long x = it.first + it.units();
     if (LIST) {
       set_list_item(a, ((long long)it.b * a.g.Hkv + it.h) * a.g.T + it.t + 1, it);
       return;
@@ -175,7 +190,7 @@ struct Walk {
     const int mts = ceil_div_i(a.G * it.ql, RT);
     const int item = it.h * mts + it.row0 / RT + 1;
     if (item < a.g.Hkv * mts) {
-      set_slot_item(a, it.first - (long long)(item - 1) * it.n_tiles, item, it);
+      set_slot_item(a, it.first - (long long)(item - 1) * it.units(), item, it);
       return;
     }
     do {
@@ -304,7 +319,7 @@ struct Parts {
   int c0, n, c1;
   __device__ Parts(const Walk<LIST, RT>& w, const Item& it) {
     c0 = w.owner(it.first);
-    c1 = w.owner(it.first + it.n_tiles - 1);
+    c1 = w.owner(it.first + it.units() - 1);
     n = c1 - c0 + 1;
   }
   __device__ size_t slot(int i) const { return 2 * (size_t)(c0 + i) + (i == 0 ? 1 : 0); }
