@@ -240,19 +240,19 @@ __global__ void __launch_bounds__(kScoreThreads, G <= 4 ? 2 : 1) page_score_kern
 
 // c += a (16x16, row) * b (16x8, col)
 template <bool F16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   if (F16)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
   else
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 // The halves of a packed pair that are below zero (neg) or not, the others 0.
@@ -284,7 +284,6 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_screen_kernel(
   const int je = min((ck + 1) * chunk, (base + t_last) / g.page + 1);   // pages up to the last token's own
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int jw = ck * chunk + warp * 8;
-  if (jw >= je) return;                         // (the whole warp)
   const int g8 = lane >> 2, tig = lane & 3;
   constexpr int kStep = (kScoreThreads / 32) * 8;
   const int32_t* table = g.table + (size_t)b * g.max_pages;
@@ -292,46 +291,56 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_screen_kernel(
     const int pg = j < je ? __ldg(table + j) : -1;
     return pg >= 0 && pg < g.n_pages ? pg : -1;
   };
-  int pg = page_of(jw + g8);                    // B column n = page jw + lane / 4
-
-  // A: rows g8 and g8 + 8 of [min(q,0), max(q,0)]. Load l, lane tig of a page row: channels
-  // 32 l + 8 tig + (0..7) of [kmin, kmax]; its words 0, 1 are the B fragment of one k16 step, words 2, 3 of
-  // the next, and A takes the same channels.
-  uint32_t af[2 * NL][4];
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = g8 + 8 * half;
-    const int t = min(t0 + r / GP, ql - 1), head = min(r % GP, G - 1);
-    const uint4* qr = reinterpret_cast<const uint4*>(q + ((((size_t)b * g.Hkv + h) * G + head) * g.T + t) * D);
-#pragma unroll
-    for (int l = 0; l < NL / 2; ++l) {
-      const uint4 w = __ldg(qr + 4 * l + tig);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {             // kmin part (q < 0), kmax part
-        const int st = 2 * (l + s * (NL / 2));
-        af[st][half] = keep_sign(w.x, s == 0);
-        af[st][2 + half] = keep_sign(w.y, s == 0);
-        af[st + 1][half] = keep_sign(w.z, s == 0);
-        af[st + 1][2 + half] = keep_sign(w.w, s == 0);
-      }
-    }
-  }
-  float* out = scores + ((size_t)bh * g.T + t0) * g.max_pages;
-  for (; jw < je; jw += kStep) {
-    uint4 v[NL];
+  auto load = [&](int pg, uint4 (&v)[NL]) {
     const uint4* bp = reinterpret_cast<const uint4*>(bounds + ((size_t)max(pg, 0) * g.Hkv + h) * 2 * D) + tig;
 #pragma unroll
     for (int l = 0; l < NL; ++l) v[l] = pg >= 0 ? __ldg(bp + 4 * l) : make_uint4(0, 0, 0, 0);
+  };
+  // B column n = page jw + lane / 4; the next step's bounds and the one after's page numbers are on
+  // their way while a step is computed
+  int pg = page_of(jw + g8), pg_next = page_of(jw + kStep + g8);
+
+  // A: rows g8 and g8 + 8 of [min(q,0), max(q,0)], in fragments. Load l, lane tig of a page row: channels
+  // 32 l + 8 tig + (0..7) of [kmin, kmax]; its words 0, 1 are the B fragment of one k16 step, words 2, 3 of
+  // the next, and A takes the same channels. A warp builds the steps of its share of the loads.
+  __shared__ uint4 af[2 * NL][32];
+  for (int l = warp; l < NL / 2; l += kScoreThreads / 32) {
+    uint4 w[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = g8 + 8 * half;
+      const int t = min(t0 + r / GP, ql - 1), head = min(r % GP, G - 1);
+      w[half] = __ldg(reinterpret_cast<const uint4*>(q + ((((size_t)b * g.Hkv + h) * G + head) * g.T + t) * D) +
+                      4 * l + tig);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {               // kmin part (q < 0), kmax part
+      const int st = 2 * (l + s * (NL / 2));
+      af[st][lane] = make_uint4(keep_sign(w[0].x, s == 0), keep_sign(w[1].x, s == 0), keep_sign(w[0].y, s == 0),
+                                keep_sign(w[1].y, s == 0));
+      af[st + 1][lane] = make_uint4(keep_sign(w[0].z, s == 0), keep_sign(w[1].z, s == 0), keep_sign(w[0].w, s == 0),
+                                    keep_sign(w[1].w, s == 0));
+    }
+  }
+  uint4 v[NL], v_next[NL];
+  load(pg, v);
+  __syncthreads();
+  float* out = scores + ((size_t)bh * g.T + t0) * g.max_pages;
+#pragma unroll 1
+  for (; jw < je; jw += kStep) {
     const bool held = pg >= 0;
-    pg = page_of(jw + kStep + g8);
+    load(pg_next, v_next);
+    pg = pg_next;
+    pg_next = page_of(jw + 2 * kStep + g8);
     float c[2][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[0][i] = c[1][i] = 0.f;
     uint32_t mx = 0;
 #pragma unroll
     for (int l = 0; l < NL; ++l) {
-      mma16816<F16>(c[0], af[2 * l], v[l].x, v[l].y);
-      mma16816<F16>(c[1], af[2 * l + 1], v[l].z, v[l].w);
+      const uint4 a0 = af[2 * l][lane], a1 = af[2 * l + 1][lane];
+      mma16816<F16>(c[0], a0, v[l].x, v[l].y);
+      mma16816<F16>(c[1], a1, v[l].z, v[l].w);
       mx = max_u16x2(mx, max_u16x2(max_u16x2(v[l].x & 0x7fff7fffu, v[l].y & 0x7fff7fffu),
                                    max_u16x2(v[l].z & 0x7fff7fffu, v[l].w & 0x7fff7fffu)));
     }
@@ -368,20 +377,23 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_screen_kernel(
         if (jw + 2 * tig + 1 < je) o[1] = r[2 * half + 1];
       }
     }
+#pragma unroll
+    for (int l = 0; l < NL; ++l) v[l] = v_next[l];
   }
 }
 
 // ---------------------------------------------------------------------------
 
-constexpr int kListThreads = 256;
+constexpr int kListThreads = 512;
+constexpr int kBins = 2048;                     // of the screen's histogram, four per thread
 constexpr int kListWarps = kListThreads / 32;
 constexpr int kWindow = 256;                    // pages near the threshold that are ranked pairwise
 
-struct ListSmem {
-  unsigned hist[256];
+struct __align__(16) ListSmem {
+  unsigned hist[kBins];
   unsigned red[kListWarps], red2[kListWarps];
   float fred[kListWarps];
-  unsigned digit, above;
+  unsigned digit, above;                        // the bin that holds the threshold, keys in bins above it
   int status;
   int n_win;                                    // pages near the threshold
   int win[kWindow];
@@ -397,18 +409,17 @@ struct Cut {
 };
 
 // Radix selection: digits of up to eight bits from the highest bit in which keys differ down; mn, mx
-// the least and the largest key; at most `digits` of them (the cut then lies within the last one's
-// range). All threads call it; keys are visible to all.
-__device__ Cut radix_cut(const uint32_t* keys, int n, int m, unsigned mn, unsigned mx, ListSmem& s, int digits) {
+// the least and the largest key. All threads call it; keys are visible to all.
+__device__ __noinline__ Cut radix_cut(const uint32_t* keys, int n, int m, unsigned mn, unsigned mx, ListSmem& s) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   Cut c{mx, 0xffffffffu, m};
   if (mn == mx) return c;
   int top = 32 - __clz(mn ^ mx);                // bits [0, top) differ
   c.mask = top == 32 ? 0u : ~((1u << top) - 1u);
   c.thr = mx & c.mask;
-  for (; top > 0 && digits > 0; --digits) {
+  while (top > 0) {
     const int sh = max(top - 8, 0), width = top - sh;
-    s.hist[tid] = 0;
+    if (tid < 256) s.hist[tid] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kListThreads) {
       const unsigned key = keys[i];
@@ -417,7 +428,7 @@ __device__ Cut radix_cut(const uint32_t* keys, int n, int m, unsigned mn, unsign
     __syncthreads();
     // thread tid: keys in digits above d, a suffix sum from the top digit down
     const int d = 255 - tid;
-    const unsigned mine = s.hist[d];
+    const unsigned mine = d >= 0 ? s.hist[d] : 0u;
     unsigned x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -442,7 +453,7 @@ __device__ Cut radix_cut(const uint32_t* keys, int n, int m, unsigned mn, unsign
 
 // s(t, j) in fp64, rounded to fp32, of one page: the whole warp. qd: the heads' scaled queries.
 template <bool F16>
-__device__ float exact_score(const uint16_t* bp, const double* qd, int G, int d) {
+__device__ __noinline__ float exact_score(const uint16_t* bp, const double* qd, int G, int d) {
   const int lane = threadIdx.x % 32;
   float best = -INFINITY;
   bool nan = false;
@@ -499,6 +510,7 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
     s.status = 0;
     s.n_win = 0;
   }
+  for (int i = tid; SCREEN && i < kBins; i += kListThreads) s.hist[i] = 0;
   if (SCREEN && ranked) {
     // a warp per head: the scaled query, and the sum of magnitudes (0 stands in for what is not
     // finite: such a query makes every score NaN, which the screen shows)
@@ -584,11 +596,40 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
 #pragma unroll
   for (int i = 0; i < kListWarps; ++i) kabs = fmaxf(kabs, s.fred[i]);
   __syncthreads();                              // red is read
-  // the screen needs the threshold to within the margin only: two digits, 2^-16 of the keys' range
-  Cut c = radix_cut(keys, n, m, mn, mx, s, SCREEN ? 2 : 4);
+  Cut c{0u, 0u, 0};
+  if (!SCREEN) c = radix_cut(keys, n, m, mn, mx, s);
 
   if (SCREEN) {
-    const float th_lo = key_score(c.thr), th_hi = key_score(c.thr | ~c.mask);
+    // the threshold to within 2^-11 of the keys' range, which the margin exceeds: one histogram of equal
+    // ranges of keys
+    const int sh = max(0, 21 - __clz(mx - mn | 1u));
+    for (int i = tid; i < n; i += kListThreads) atomicAdd(&s.hist[(keys[i] - mn) >> sh], 1u);
+    __syncthreads();
+    // thread tid: the bins 4 d .. 4 d + 3 and the keys above them, from the top down
+    const int d = kBins / 4 - 1 - tid;
+    const uint4 h4 = *reinterpret_cast<const uint4*>(&s.hist[4 * d]);
+    const unsigned mine = h4.x + h4.y + h4.z + h4.w;
+    unsigned x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s.red[warp] = x;
+    __syncthreads();
+    unsigned above = x - mine;
+    for (int i = 0; i < warp; ++i) above += s.red[i];
+    const unsigned um = (unsigned)m;
+    if (above < um && above + mine >= um) {
+      unsigned at = above, bin = 4 * d + 3;
+      if (at + h4.w < um) { at += h4.w; --bin;
+        if (at + h4.z < um) { at += h4.z; --bin;
+          if (at + h4.y < um) { at += h4.y; --bin; } } }
+      s.digit = bin;
+    }
+    __syncthreads();
+    const unsigned klo = mn + (s.digit << sh), khi = klo + ((1u << sh) - 1u);
+    const float th_lo = key_score(klo), th_hi = key_score(min(khi, mx));
     // 2^-14 for the sums; what 16-bit subnormals could lose if an MMA flushed them
     const float delta = 0x1p-14f * q1 * kabs + (F16 ? 0x1p-13f : 0x1p-100f) * (q1 + g.d * kabs);
     const float lo = th_lo - 2.f * delta, hi = th_hi + 2.f * delta;
@@ -651,7 +692,7 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
         if (lane == 0) keys[i] = exact;
       }
       __syncthreads();
-      c = radix_cut(keys, n, m, 0u, 0xffffffffu, s, 4);
+      c = radix_cut(keys, n, m, 0u, 0xffffffffu, s);
     }
     __syncthreads();
   }
