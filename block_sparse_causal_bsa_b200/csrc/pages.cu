@@ -125,13 +125,14 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(int slots, int max_page
 
 constexpr int kResizeThreads = 1024;
 
-struct ResizeSmem {
+struct __align__(16) ResizeSmem {
+  int tail[kMaxSlots];                   // shared last page of a growing slot, or -1 (read four at a time)
+  int first[kMaxSlots + 1];              // exclusive prefix of the pages given up, then of the pages needed
+  int len[kMaxSlots], want[kMaxSlots];   // before and after (want = len: left as it is)
+  uint8_t flags[kMaxSlots];              // 1 grows, 2 copy on write, 4 keeps a shared page, 8 granted
   int warp_sum[32];
   int status;
   int taken;                             // pages given out
-  int first[kMaxSlots + 1];              // exclusive prefix of the pages needed
-  int tail[kMaxSlots];                   // shared last page of a growing slot, or -1
-  uint8_t flags[kMaxSlots];              // 1 grows, 2 copy on write, 4 keeps a shared page, 8 granted
 };
 
 // Exclusive prefix of one value per thread; *total gets the sum. All threads call it.
@@ -161,47 +162,88 @@ __device__ int block_exclusive(int v, int* warp_sum, int* total) {
   return r;
 }
 
+// Prefix of per-slot counts count(t) into s.first, in slot order; returns the total. All threads.
+template <class F>
+__device__ int slot_prefix(ResizeSmem& s, int slots, F count) {
+  const int per = ceil_div(slots, kResizeThreads);
+  const int t0 = min((int)threadIdx.x * per, slots), t1 = min(t0 + per, slots);
+  int mine = 0;
+  for (int t = t0; t < t1; ++t) {
+    const int c = count(t);
+    s.first[t] = c;
+    mine += c;
+  }
+  int total;
+  int at = block_exclusive(mine, s.warp_sum, &total);
+  for (int t = t0; t < t1; ++t) {
+    const int c = s.first[t];
+    s.first[t] = at;
+    at += c;
+  }
+  if (threadIdx.x == 0) s.first[slots] = total;
+  __syncthreads();
+  return total;
+}
+
+// The slot whose range of s.first holds i.
+__device__ __forceinline__ int slot_of(const ResizeSmem& s, int slots, int i) {
+  int lo = 0, hi = slots;                // first[lo] <= i < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (s.first[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Everything per slot sits in shared memory after one coalesced read, and every loop over pages runs
+// one page per thread, whatever slot it belongs to: the kernel is a chain of some ten barriers and
+// five memory latencies. (A warp per slot took 35 us for 504 slots.)
 __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(
     int slots, int max_pages, int n_pages, int page, int32_t* table, int32_t* seq_len, int32_t* refs,
     const int32_t* __restrict__ new_len, int32_t* __restrict__ pairs, int32_t* n_free, int32_t* dev_status) {
   extern __shared__ __align__(16) uint8_t raw[];
   ResizeSmem& s = *reinterpret_cast<ResizeSmem*>(raw);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int tid = threadIdx.x;
   const long long max_len = (long long)max_pages * page;
   if (tid == 0) s.status = s.taken = 0;
   __syncthreads();
-
-  // 1. shrinking slots give up pages (a warp per slot)
-  for (int t = warp; t < slots; t += kResizeThreads / 32) {
+  for (int t = tid; t < slots; t += kResizeThreads) {
     const int L = seq_len[t], n = new_len[t];
     const bool ok = L >= 0 && L <= max_len && n <= max_len;
-    if (!ok && lane == 0) atomicOr(&s.status, BSA_DEV_BAD_INDEX);
-    if (lane == 0) s.flags[t] = ok && n > L ? 1 : 0;
-    if (ok && n >= 0 && n < L) {
-      for (int j = ceil_div(n, page) + lane; j < ceil_div(L, page); j += 32) {
-        int32_t* e = table + (size_t)t * max_pages + j;
-        const int pg = *e;
-        *e = -1;
-        if (pg < 0 || pg >= n_pages) {
-          atomicOr(&s.status, BSA_DEV_BAD_INDEX);
-        } else if (atomicSub(refs + pg, 1) <= 0) {
-          atomicAdd(refs + pg, 1);       // was not held: leave the count as it was
-          atomicOr(&s.status, BSA_DEV_BAD_INDEX);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) seq_len[t] = n;
+    if (!ok) atomicOr(&s.status, BSA_DEV_BAD_INDEX);
+    s.len[t] = ok ? L : 0;
+    s.want[t] = ok ? (n < 0 ? L : n) : 0;
+    s.flags[t] = ok && n > L ? 1 : 0;
+  }
+  __syncthreads();
+
+  // 1. shrinking slots give up pages
+  const int dropped = slot_prefix(s, slots, [&](int t) {
+    return max(ceil_div(s.len[t], page) - ceil_div(s.want[t], page), 0);
+  });
+  for (int i = tid; i < dropped; i += kResizeThreads) {
+    const int t = slot_of(s, slots, i);
+    int32_t* e = table + (size_t)t * max_pages + ceil_div(s.want[t], page) + i - s.first[t];
+    const int pg = *e;
+    *e = -1;
+    if (pg < 0 || pg >= n_pages) {
+      atomicOr(&s.status, BSA_DEV_BAD_INDEX);
+    } else if (atomicSub(refs + pg, 1) <= 0) {
+      atomicAdd(refs + pg, 1);           // was not held: leave the count as it was
+      atomicOr(&s.status, BSA_DEV_BAD_INDEX);
     }
   }
   __threadfence();
   __syncthreads();
 
-  // 2. growing slots whose partly filled last page has other holders
-  for (int t = tid; t < slots; t += kResizeThreads) {
+  // 2. growing slots whose partly filled last page has other holders (shrinking slots set their length)
+  for (int t = tid; t < kMaxSlots; t += kResizeThreads) {
     int tail = -1;
-    if (s.flags[t] & 1) {
-      const int L = seq_len[t];
-      if (L % page) {
+    if (t < slots) {
+      const int L = s.len[t];
+      if (s.want[t] < L) seq_len[t] = s.want[t];
+      if ((s.flags[t] & 1) && L % page) {
         const int pg = table[(size_t)t * max_pages + L / page];
         if (pg < 0 || pg >= n_pages) {
           atomicOr(&s.status, BSA_DEV_BAD_INDEX);
@@ -220,51 +262,41 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(
   for (int t = tid; t < slots; t += kResizeThreads) {
     const int pg = s.tail[t];
     if (pg < 0) continue;
-    int holders = 0;
-    bool later = false;
-    for (int u = 0; u < slots; ++u) {
-      if (s.tail[u] == pg) {
-        ++holders;
-        later |= u > t;
-      }
+    int holders = 0, last = 0;
+    for (int u = 0; u < slots; u += 4) {           // (tail is -1 past the slots)
+      const int4 v = *reinterpret_cast<const int4*>(s.tail + u);
+      holders += (v.x == pg) + (v.y == pg) + (v.z == pg) + (v.w == pg);
+      if (v.x == pg) last = u;
+      if (v.y == pg) last = u + 1;
+      if (v.z == pg) last = u + 2;
+      if (v.w == pg) last = u + 3;
     }
-    s.flags[t] |= (holders == __ldcg(refs + pg) && !later) ? 4 : 2;
+    s.flags[t] |= (holders == __ldcg(refs + pg) && last == t) ? 4 : 2;
   }
   __syncthreads();
 
   // 3. pages needed per slot, in slot order
-  const int per = ceil_div(slots, kResizeThreads);
-  const int t0 = min(tid * per, slots), t1 = min(t0 + per, slots);
-  int mine = 0;
-  for (int t = t0; t < t1; ++t) {
-    int need = 0;
-    if (s.flags[t] & 1) {
-      need = ceil_div(new_len[t], page) - ceil_div(seq_len[t], page) + ((s.flags[t] >> 1) & 1);
-    }
-    s.first[t] = need;
-    mine += need;
-  }
-  int total;
-  int at = block_exclusive(mine, s.warp_sum, &total);
-  for (int t = t0; t < t1; ++t) {
-    const int need = s.first[t];
-    s.first[t] = at;
-    at += need;
-  }
-  if (tid == 0) s.first[slots] = total;
+  const int total = slot_prefix(s, slots, [&](int t) {
+    return s.flags[t] & 1 ? ceil_div(s.want[t], page) - ceil_div(s.len[t], page) + ((s.flags[t] >> 1) & 1) : 0;
+  });
 
   // 4. free pages: a contiguous range of the pool per thread (rounded to a multiple of four,
   // so that it is read 16 bytes at a time), counted, then given out lowest first
   const int seg = ceil_div(ceil_div(n_pages, kResizeThreads), 4) * 4;
-  const int p0 = min((long long)tid * seg, (long long)n_pages), p1 = min(p0 + seg, n_pages);
+  const int p0 = (int)min((long long)tid * seg, (long long)n_pages), p1 = min(p0 + seg, n_pages);
+  auto counts = [&](int p) {             // of pages p .. p + 3; 1 past the end
+    if (p + 4 <= p1) return __ldcg(reinterpret_cast<const int4*>(refs + p));
+    int4 r = make_int4(1, 1, 1, 1);
+    if (p < p1) r.x = __ldcg(refs + p);
+    if (p + 1 < p1) r.y = __ldcg(refs + p + 1);
+    if (p + 2 < p1) r.z = __ldcg(refs + p + 2);
+    return r;
+  };
   int free_here = 0;
+#pragma unroll 4
   for (int p = p0; p < p1; p += 4) {
-    if (p + 4 <= p1) {
-      const int4 r = __ldcg(reinterpret_cast<const int4*>(refs + p));
-      free_here += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
-    } else {
-      for (int i = p; i < p1; ++i) free_here += __ldcg(refs + i) == 0;
-    }
+    const int4 r = counts(p);
+    free_here += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
   }
   int avail;
   int rank = block_exclusive(free_here, s.warp_sum, &avail);
@@ -279,33 +311,29 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(
     }
   }
   __syncthreads();
-  for (int p = p0; p < p1 && rank < total; ++p) {
-    if (__ldcg(refs + p) != 0) continue;
-    const int r = rank++;
-    // the slot whose pages include rank r: the last one with first <= r and need > 0
-    int lo = 0, hi = slots;              // first[lo] <= r < first[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (s.first[mid] <= r) lo = mid;
-      else hi = mid;
-    }
-    if (!(s.flags[lo] & 8)) continue;
-    const int i = r - s.first[lo], cow = (s.flags[lo] >> 1) & 1;
-    const int L = seq_len[lo];
-    refs[p] = 1;
-    if (cow && i == 0) {
-      int32_t* e = table + (size_t)lo * max_pages + L / page;
-      pairs[2 * lo] = *e;
-      pairs[2 * lo + 1] = p;
-      atomicSub(refs + *e, 1);           // stays above 0: another holder keeps the page
-      *e = p;
-    } else {
-      table[(size_t)lo * max_pages + ceil_div(L, page) + i - cow] = p;
+  for (int p = p0; p < p1 && rank < total; p += 4) {
+    const int4 r4 = counts(p);
+    const int c4[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (c4[k] != 0 || rank >= total) continue;
+      const int r = rank++, pg = p + k;
+      const int t = slot_of(s, slots, r);          // (the last slot with first <= r: it needs pages)
+      if (!(s.flags[t] & 8)) continue;
+      const int i = r - s.first[t], cow = (s.flags[t] >> 1) & 1, L = s.len[t];
+      refs[pg] = 1;
+      if (cow && i == 0) {
+        pairs[2 * t] = s.tail[t];
+        pairs[2 * t + 1] = pg;
+        atomicSub(refs + s.tail[t], 1);            // stays above 0: another holder keeps the page
+        table[(size_t)t * max_pages + L / page] = pg;
+      } else {
+        table[(size_t)t * max_pages + ceil_div(L, page) + i - cow] = pg;
+      }
     }
   }
-  __syncthreads();                       // seq_len is read above
   for (int t = tid; t < slots; t += kResizeThreads) {
-    if (s.flags[t] & 8) seq_len[t] = new_len[t];
+    if (s.flags[t] & 8) seq_len[t] = s.want[t];
     if ((s.flags[t] & 10) != 10) pairs[2 * t] = pairs[2 * t + 1] = -1;
   }
   if (tid == 0) {
@@ -548,7 +576,9 @@ cudaError_t launch_pages_fork(int slots, int max_pages, int n_pages, int page, i
 cudaError_t launch_pages_resize(int slots, int max_pages, int n_pages, int page, int32_t* table,
                                 int32_t* seq_len, int32_t* refs, const int32_t* new_len, int32_t* pairs,
                                 int32_t* n_free, int32_t* dev_status, cudaStream_t st) {
-  static_assert(sizeof(ResizeSmem) <= 48 * 1024, "resize shared memory");
+  static SmemSet set;
+  cudaError_t e = allow_smem((const void*)pages_resize_kernel, sizeof(ResizeSmem), set);
+  if (e != cudaSuccess) return e;
   pages_resize_kernel<<<1, kResizeThreads, sizeof(ResizeSmem), st>>>(
       slots, max_pages, n_pages, page, table, seq_len, refs, new_len, pairs, n_free, dev_status);
   return cudaGetLastError();

@@ -298,8 +298,8 @@ def _query(q, cache):
     return Hq, T, _tensor("q", q, (cache.slots, Hq, T, d), cache.k.dtype, cache.device)
 
 
-def _attend(name, q, cache, extra, q_len, layer, scale, out, lse, stream):
-    Hq, T, qp = _query(q, cache)
+def _attend(name, q, query, cache, extra, q_len, layer, scale, out, lse, stream):
+    Hq, T, qp = query
     ql = _qlen(cache, q_len)
     k, v, _ = cache._layer(layer)
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
@@ -329,25 +329,26 @@ def attend_tree(q: torch.Tensor, cache: PagedCache, *, mask=None, q_len=None, la
     """Attention of the last q_len positions (q [slots, Hq, T, d]) over the whole cache of their
     slots; mask int64 [slots, T, ceil(T/64)] says which drafted tokens see each other (None: a
     chain). Returns (out, lse, status)."""
+    query = _query(q, cache)
     m = None
     if mask is not None:
-        _, T, _ = _query(q, cache)
+        T = query[1]
         m = _tensor("mask", mask, (cache.slots, T, (T + 63) // 64), torch.int64, cache.device)
-    return _attend("bsa_attend_tree", q, cache, (m,), q_len, layer, scale, out, lse, stream)
+    return _attend("bsa_attend_tree", q, query, cache, (m,), q_len, layer, scale, out, lse, stream)
 
 
 def attend_pages(q: torch.Tensor, cache: PagedCache, kv_idx: torch.Tensor, kv_cnt: torch.Tensor, *,
                  q_len=None, layer: int = 0, scale: Optional[float] = None, out=None, lse=None, stream=None):
     """Attention of each token over its listed pages (kv_idx [slots, Hkv, T, W], kv_cnt [slots, Hkv,
     T], int32). Returns (out, lse, status)."""
-    _, T, _ = _query(q, cache)
-    H = cache.k.shape[2]
+    query = _query(q, cache)
+    T, H = query[1], cache.k.shape[2]
     if not isinstance(kv_idx, torch.Tensor) or kv_idx.dim() != 4:
         _bad("kv_idx must be [slots, Hkv, T, W]")
     W = kv_idx.shape[3]
     i = _tensor("kv_idx", kv_idx, (cache.slots, H, T, W), torch.int32, cache.device)
     c = _tensor("kv_cnt", kv_cnt, (cache.slots, H, T), torch.int32, cache.device)
-    return _attend("bsa_attend_pages", q, cache, (i, c, W), q_len, layer, scale, out, lse, stream)
+    return _attend("bsa_attend_pages", q, query, cache, (i, c, W), q_len, layer, scale, out, lse, stream)
 
 
 def select_pages(q: torch.Tensor, cache: PagedCache, cfg: PageSelectConfig, *, q_len=None, layer: int = 0,
