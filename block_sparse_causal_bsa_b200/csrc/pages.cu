@@ -222,15 +222,32 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(
   const int dropped = slot_prefix(s, slots, [&](int t) {
     return max(ceil_div(s.len[t], page) - ceil_div(s.want[t], page), 0);
   });
-  for (int i = tid; i < dropped; i += kResizeThreads) {
-    const int t = slot_of(s, slots, i);
-    int32_t* e = table + (size_t)t * max_pages + ceil_div(s.want[t], page) + i - s.first[t];
-    const int pg = *e;
-    *e = -1;
-    if (pg < 0 || pg >= n_pages) {
-      atomicOr(&s.status, BSA_DEV_BAD_INDEX);
-    } else if (atomicSub(refs + pg, 1) <= 0) {
-      atomicAdd(refs + pg, 1);           // was not held: leave the count as it was
+  constexpr int kU = 4;                  // pages of a thread in flight
+  for (int i0 = tid; i0 < dropped; i0 += kU * kResizeThreads) {
+    int32_t* e[kU];
+    int pg[kU], held[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int i = i0 + u * kResizeThreads;
+      e[u] = nullptr;
+      if (i < dropped) {
+        const int t = slot_of(s, slots, i);
+        e[u] = table + (size_t)t * max_pages + ceil_div(s.want[t], page) + i - s.first[t];
+      }
+      pg[u] = e[u] ? *e[u] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      held[u] = 1;
+      if (!e[u]) continue;
+      *e[u] = -1;
+      if (pg[u] < 0 || pg[u] >= n_pages) atomicOr(&s.status, BSA_DEV_BAD_INDEX);
+      else held[u] = atomicSub(refs + pg[u], 1);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (held[u] > 0) continue;
+      atomicAdd(refs + pg[u], 1);        // was not held: leave the count as it was
       atomicOr(&s.status, BSA_DEV_BAD_INDEX);
     }
   }

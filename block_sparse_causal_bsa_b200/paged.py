@@ -22,8 +22,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import dataclasses
-import math
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -35,6 +34,21 @@ _DTYPES = {torch.bfloat16: BSA_BF16, torch.float16: BSA_F16}
 
 def _bad(msg: str, status: int = BSA_ERR_INVALID_ARG):
     raise BsaError(status, msg)
+
+
+class _Plan(NamedTuple):
+    """What a cache's tensors say, read once (a step makes several calls per layer)."""
+    shape: object
+    layers: int
+    Hkv: int
+    page: int
+    d: int
+    dtype: torch.dtype
+    device: torch.device
+    index: Optional[int]
+    slots: int
+    max_pages: int
+    row_bytes: int                   # of one row per page of a layer
 
 
 @dataclasses.dataclass
@@ -97,16 +111,21 @@ class PagedCache:
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         if not name.startswith("_"):             # what is derived from the tensors is derived anew
-            object.__setattr__(self, "_shape", None)
+            object.__setattr__(self, "_plan", None)
             object.__setattr__(self, "_bytes", {})
 
     def shape(self):
         """The C shape (by reference), kept until a tensor of the cache is replaced."""
-        if self._shape is None:
-            self._check()
-            _, P, H, page, d = self.k.shape
-            self._shape = ctypes.byref(CacheShape(P, H, page, d, _DTYPES[self.k.dtype]))
-        return self._shape
+        return (self._plan or self._make_plan()).shape
+
+    def _make_plan(self):
+        self._check()
+        L, P, H, page, d = self.k.shape
+        dev = self.k.device
+        self._plan = _Plan(ctypes.byref(CacheShape(P, H, page, d, _DTYPES[self.k.dtype])), L, H, page, d,
+                           self.k.dtype, dev, dev.index if dev.type == "cuda" else None,
+                           self.page_table.shape[0], self.page_table.shape[1], P * H * d * 2)
+        return self._plan
 
     def workspace_bytes(self, call: str, Hq: int, T: int) -> int:
         n = self._bytes.get((call, Hq, T))
@@ -117,20 +136,13 @@ class PagedCache:
             self._bytes[(call, Hq, T)] = n
         return n
 
-    def _scratch(self, nbytes: int) -> torch.Tensor:
-        return self.refs.new_empty((nbytes + 3) // 4)
 
-    def _layer(self, layer: int):
-        L, P, H, page, d = self.k.shape
-        if not 0 <= layer < L:
-            _bad(f"layer {layer} of {L}")
-        step = layer * P * H * d * 2
-        return (self.k.data_ptr() + step * page, self.v.data_ptr() + step * page,
+    def _layer(self, p, layer: int):
+        if not 0 <= layer < p.layers:
+            _bad(f"layer {layer} of {p.layers}")
+        step = layer * p.row_bytes
+        return (self.k.data_ptr() + step * p.page, self.v.data_ptr() + step * p.page,
                 self.bounds.data_ptr() + 2 * step if self.bounds is not None else None)
-
-    def _table(self):
-        self.shape()
-        return self.slots, self.max_pages, self.k.shape[1], self.k.shape[3]
 
 
 @dataclasses.dataclass
@@ -156,80 +168,79 @@ def _tensor(name: str, t, shape, dtype, device):
     _bad(f"{name} must be contiguous")
 
 
-class _On:
-    """Run on the device, outputs and workspaces allocated for the stream that uses them; gives
-    the stream's handle. A step makes several of these calls per layer, so the usual case (the
-    current device and stream) takes no context switch."""
-    __slots__ = ("device", "stream", "inner")
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            _bad(f"the cache is on {device}; the kernels need a GPU")
-        self.device, self.stream, self.inner = device, stream, None
-
-    def __enter__(self):
-        idx = self.device.index
-        if self.stream is None and torch._C._cuda_getDevice() == idx:
-            return torch._C._cuda_getCurrentRawStream(idx)
-        self.inner = contextlib.ExitStack()
-        self.inner.enter_context(torch.cuda.device(self.device))
-        if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
-        st = torch.cuda.ExternalStream(self.stream) if isinstance(self.stream, int) else self.stream
-        self.inner.enter_context(torch.cuda.stream(st))
-        return st.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.close()
-        return False
+def _stream(p, stream):
+    """The handle of the current stream, when the call is to run there; None: it needs _elsewhere."""
+    if p.index is None:
+        _bad(f"the cache is on {p.device}; the kernels need a GPU")
+    if stream is None and torch._C._cuda_getDevice() == p.index:
+        return torch._C._cuda_getCurrentRawStream(p.index)
+    return None
 
 
-def _status(like):
-    return like.new_empty(1)
+def _elsewhere(p, stream, call, *args, **kw):
+    """call(*args, **kw) with the cache's device and `stream` current, so that outputs and
+    workspaces are allocated for the stream that uses them."""
+    with contextlib.ExitStack() as st:
+        st.enter_context(torch.cuda.device(p.device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=p.device)
+            if stream.device != p.device:
+                _bad(f"the stream is on {stream.device}, the cache on {p.device}")
+            st.enter_context(torch.cuda.stream(stream))
+        return call(*args, **kw)
 
 
-def _qlen(cache, q_len):
-    return None if q_len is None else _tensor("q_len", q_len, (cache.slots,), torch.int32, cache.device)
+def _qlen(cache, p, q_len):
+    return None if q_len is None else _tensor("q_len", q_len, (p.slots,), torch.int32, p.device)
 
 
 def fork(cache: PagedCache, parent: torch.Tensor, *, stream=None) -> torch.Tensor:
     """Slots c with parent[c] >= 0 (int32 [slots]) become copies of their parents, sharing their
     pages. Returns the status."""
-    p = _tensor("parent", parent, (cache.slots,), torch.int32, cache.device)
-    with _On(cache.device, stream) as s:
-        st = _status(cache.refs)
-        _check(lib().bsa_pages_fork(*cache._table(), cache.page_table.data_ptr(), cache.seq_len.data_ptr(),
-                                    cache.refs.data_ptr(), p, st.data_ptr(), s))
+    p = cache._plan or cache._make_plan()
+    pp = _tensor("parent", parent, (p.slots,), torch.int32, p.device)
+    s = _stream(p, stream)
+    if s is None:
+        return _elsewhere(p, stream, fork, cache, parent)
+    refs = cache.refs
+    st = refs.new_empty(1)
+    _check(lib().bsa_pages_fork(p.slots, p.max_pages, refs.shape[0], p.page, cache.page_table.data_ptr(),
+                                cache.seq_len.data_ptr(), refs.data_ptr(), pp, st.data_ptr(), s))
     return st
 
 
 def resize(cache: PagedCache, new_len: torch.Tensor, *, stream=None):
     """Sets the slots' lengths (int32 [slots]; negative: as it is, 0: freed), taking and giving up
     pages. Returns (pairs [slots, 2] for copy_pages, free pages left, status)."""
-    n = _tensor("new_len", new_len, (cache.slots,), torch.int32, cache.device)
-    with _On(cache.device, stream) as s:
-        st, n_free = _status(cache.refs), _status(cache.refs)
-        pairs = cache.refs.new_empty(cache.slots, 2)
-        _check(lib().bsa_pages_resize(*cache._table(), cache.page_table.data_ptr(),
-                                      cache.seq_len.data_ptr(), cache.refs.data_ptr(), n, pairs.data_ptr(),
-                                      n_free.data_ptr(), st.data_ptr(), s))
+    p = cache._plan or cache._make_plan()
+    n = _tensor("new_len", new_len, (p.slots,), torch.int32, p.device)
+    s = _stream(p, stream)
+    if s is None:
+        return _elsewhere(p, stream, resize, cache, new_len)
+    refs = cache.refs
+    st, n_free, pairs = refs.new_empty(1), refs.new_empty(1), refs.new_empty(p.slots, 2)
+    _check(lib().bsa_pages_resize(p.slots, p.max_pages, refs.shape[0], p.page, cache.page_table.data_ptr(),
+                                  cache.seq_len.data_ptr(), refs.data_ptr(), n, pairs.data_ptr(),
+                                  n_free.data_ptr(), st.data_ptr(), s))
     return pairs, n_free, st
 
 
 def copy_pages(cache: PagedCache, pairs: torch.Tensor, *, layer: int = 0, stream=None) -> torch.Tensor:
     """Copies one layer's pages pairs[i, 0] to pairs[i, 1] (int32 [n, 2]; (-1, -1) is skipped).
     Returns the status."""
+    p = cache._plan or cache._make_plan()
     if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2:
         _bad("pairs must be [n, 2]")
-    p = _tensor("pairs", pairs, (pairs.shape[0], 2), torch.int32, cache.device)
-    k, v, b = cache._layer(layer)
-    shape = cache.shape()
-    with _On(cache.device, stream) as s:
-        st = _status(cache.refs)
-        if pairs.shape[0] == 0:
-            return st.zero_()
-        _check(lib().bsa_pages_copy(shape, k, v, b, p, pairs.shape[0], st.data_ptr(), s))
+    pp = _tensor("pairs", pairs, (pairs.shape[0], 2), torch.int32, p.device)
+    k, v, b = cache._layer(p, layer)
+    s = _stream(p, stream)
+    if s is None:
+        return _elsewhere(p, stream, copy_pages, cache, pairs, layer=layer)
+    st = cache.refs.new_empty(1)
+    if pairs.shape[0] == 0:
+        return st.zero_()
+    _check(lib().bsa_pages_copy(p.shape, k, v, b, pp, pairs.shape[0], st.data_ptr(), s))
     return st
 
 
@@ -237,20 +248,21 @@ def append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, *, q_len
            stream=None) -> torch.Tensor:
     """Writes k_new, v_new [slots, Hkv, T, d] to the last q_len positions of the slots (resize
     comes first) and extends their pages' bounds. Returns the status."""
-    _, _, H, _, d = cache.k.shape
+    p = cache._plan or cache._make_plan()
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
         _bad("k_new must be [slots, Hkv, T, d]")
     T = k_new.shape[2]
-    kn = _tensor("k_new", k_new, (cache.slots, H, T, d), cache.k.dtype, cache.device)
-    vn = _tensor("v_new", v_new, (cache.slots, H, T, d), cache.k.dtype, cache.device)
-    ql = _qlen(cache, q_len)
-    k, v, b = cache._layer(layer)
-    shape = cache.shape()
-    with _On(cache.device, stream) as s:
-        st = _status(cache.refs)
-        _check(lib().bsa_cache_append(shape, cache.slots, cache.max_pages, T, kn, vn, k, v, b,
-                                      cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
-                                      st.data_ptr(), s))
+    shape = (p.slots, p.Hkv, T, p.d)
+    kn = _tensor("k_new", k_new, shape, p.dtype, p.device)
+    vn = _tensor("v_new", v_new, shape, p.dtype, p.device)
+    ql = _qlen(cache, p, q_len)
+    k, v, b = cache._layer(p, layer)
+    s = _stream(p, stream)
+    if s is None:
+        return _elsewhere(p, stream, append, cache, k_new, v_new, q_len=q_len, layer=layer)
+    st = cache.refs.new_empty(1)
+    _check(lib().bsa_cache_append(p.shape, p.slots, p.max_pages, T, kn, vn, k, v, b, cache.page_table.data_ptr(),
+                                  cache.seq_len.data_ptr(), ql, st.data_ptr(), s))
     return st
 
 
@@ -258,19 +270,20 @@ def compact(cache: PagedCache, keep: torch.Tensor, n_keep: torch.Tensor, *, q_le
             stream=None) -> torch.Tensor:
     """Moves the rows keep[s, :n_keep[s]] (ascending, int32 [slots, T]) of the last q_len positions
     of each slot together. Resize to seq_len - q_len + n_keep afterwards. Returns the status."""
+    p = cache._plan or cache._make_plan()
     if not isinstance(keep, torch.Tensor) or keep.dim() != 2:
         _bad("keep must be [slots, T]")
     T = keep.shape[1]
-    kp = _tensor("keep", keep, (cache.slots, T), torch.int32, cache.device)
-    nk = _tensor("n_keep", n_keep, (cache.slots,), torch.int32, cache.device)
-    ql = _qlen(cache, q_len)
-    k, v, b = cache._layer(layer)
-    shape = cache.shape()
-    with _On(cache.device, stream) as s:
-        st = _status(cache.refs)
-        _check(lib().bsa_cache_compact(shape, cache.slots, cache.max_pages, T, kp, nk, k, v, b,
-                                       cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
-                                       st.data_ptr(), s))
+    kp = _tensor("keep", keep, (p.slots, T), torch.int32, p.device)
+    nk = _tensor("n_keep", n_keep, (p.slots,), torch.int32, p.device)
+    ql = _qlen(cache, p, q_len)
+    k, v, b = cache._layer(p, layer)
+    s = _stream(p, stream)
+    if s is None:
+        return _elsewhere(p, stream, compact, cache, keep, n_keep, q_len=q_len, layer=layer)
+    st = cache.refs.new_empty(1)
+    _check(lib().bsa_cache_compact(p.shape, p.slots, p.max_pages, T, kp, nk, k, v, b, cache.page_table.data_ptr(),
+                                   cache.seq_len.data_ptr(), ql, st.data_ptr(), s))
     return st
 
 
@@ -281,46 +294,54 @@ def tree_mask(parents: torch.Tensor, *, q_len=None, stream=None):
         _bad("parents must be [B, T]")
     B, T = parents.shape
     dev = parents.device
-    p = _tensor("parents", parents, (B, T), torch.int32, dev)
+    pp = _tensor("parents", parents, (B, T), torch.int32, dev)
     ql = None if q_len is None else _tensor("q_len", q_len, (B,), torch.int32, dev)
-    with _On(dev, stream) as s:
-        st = _status(parents)
-        mask = torch.empty(B, T, (T + 63) // 64, dtype=torch.int64, device=dev)
-        _check(lib().bsa_tree_mask(B, T, p, ql, mask.data_ptr(), st.data_ptr(), s))
+    where = _Where(dev, dev.index if dev.type == "cuda" else None)
+    s = _stream(where, stream)
+    if s is None:
+        return _elsewhere(where, stream, tree_mask, parents, q_len=q_len)
+    st = parents.new_empty(1)
+    mask = parents.new_empty(B, T, (T + 63) // 64, dtype=torch.int64)
+    _check(lib().bsa_tree_mask(B, T, pp, ql, mask.data_ptr(), st.data_ptr(), s))
     return mask, st
 
 
-def _query(q, cache):
-    _, _, H, _, d = cache.k.shape
+class _Where(NamedTuple):
+    device: torch.device
+    index: Optional[int]
+
+
+def _query(q, p):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         _bad("q must be [slots, Hq, T, d]")
-    Hq, T = q.shape[1], q.shape[2]
-    return Hq, T, _tensor("q", q, (cache.slots, Hq, T, d), cache.k.dtype, cache.device)
+    _, Hq, T, _ = q.shape
+    return Hq, T, _tensor("q", q, (p.slots, Hq, T, p.d), p.dtype, p.device)
 
 
-def _attend(name, q, query, cache, extra, q_len, layer, scale, out, lse, stream):
+def _attend(call, q, query, cache, p, extra, q_len, layer, scale, out, lse, s):
     Hq, T, qp = query
-    ql = _qlen(cache, q_len)
-    k, v, _ = cache._layer(layer)
-    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
-    if out is not None:
-        _tensor("out", out, q.shape, q.dtype, cache.device)
-    if lse is not None:
-        _tensor("lse", lse, q.shape[:3], torch.float32, cache.device)
-    shape = cache.shape()
-    with _On(cache.device, stream) as s:
-        st = _status(cache.refs)
-        # rows past q_len are not written: 0 and -inf in tensors made here
-        if out is None:
-            out = torch.empty_like(q) if q_len is None else torch.zeros_like(q)
-        if lse is None:
-            lse = torch.full(q.shape[:3], float("-inf"), dtype=torch.float32, device=q.device) \
-                if q_len is not None else torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-        nb = cache.workspace_bytes("attend_paged", Hq, T)
-        ws = cache._scratch(nb)
-        _check(getattr(lib(), name)(shape, cache.slots, cache.max_pages, Hq, T, qp, k, v,
-                                    cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql, *extra, scale,
-                                    out.data_ptr(), lse.data_ptr(), st.data_ptr(), ws.data_ptr(), nb, s))
+    ql = _qlen(cache, p, q_len)
+    k, v, _ = cache._layer(p, layer)
+    if scale is None:
+        scale = p.d ** -0.5
+    nb = cache.workspace_bytes("attend_paged", Hq, T)
+    # rows past q_len are not written: 0 and -inf in tensors made here
+    if out is None:
+        out = torch.empty_like(q) if q_len is None else torch.zeros_like(q)
+        op = out.data_ptr()
+    else:
+        op = _tensor("out", out, q.shape, q.dtype, p.device)
+    if lse is None:
+        lse = q.new_empty(q.shape[:3], dtype=torch.float32)
+        if q_len is not None:
+            lse.fill_(float("-inf"))
+        lp = lse.data_ptr()
+    else:
+        lp = _tensor("lse", lse, q.shape[:3], torch.float32, p.device)
+    refs = cache.refs
+    st, ws = refs.new_empty(1), refs.new_empty((nb + 3) // 4)
+    _check(call(p.shape, p.slots, p.max_pages, Hq, T, qp, k, v, cache.page_table.data_ptr(),
+                cache.seq_len.data_ptr(), ql, *extra, scale, op, lp, st.data_ptr(), ws.data_ptr(), nb, s))
     return out, lse, st
 
 
@@ -329,26 +350,36 @@ def attend_tree(q: torch.Tensor, cache: PagedCache, *, mask=None, q_len=None, la
     """Attention of the last q_len positions (q [slots, Hq, T, d]) over the whole cache of their
     slots; mask int64 [slots, T, ceil(T/64)] says which drafted tokens see each other (None: a
     chain). Returns (out, lse, status)."""
-    query = _query(q, cache)
+    p = cache._plan or cache._make_plan()
+    query = _query(q, p)
     m = None
     if mask is not None:
         T = query[1]
-        m = _tensor("mask", mask, (cache.slots, T, (T + 63) // 64), torch.int64, cache.device)
-    return _attend("bsa_attend_tree", q, query, cache, (m,), q_len, layer, scale, out, lse, stream)
+        m = _tensor("mask", mask, (p.slots, T, (T + 63) // 64), torch.int64, p.device)
+    s = _stream(p, stream)
+    if s is None:
+        return _elsewhere(p, stream, attend_tree, q, cache, mask=mask, q_len=q_len, layer=layer, scale=scale,
+                          out=out, lse=lse)
+    return _attend(lib().bsa_attend_tree, q, query, cache, p, (m,), q_len, layer, scale, out, lse, s)
 
 
 def attend_pages(q: torch.Tensor, cache: PagedCache, kv_idx: torch.Tensor, kv_cnt: torch.Tensor, *,
                  q_len=None, layer: int = 0, scale: Optional[float] = None, out=None, lse=None, stream=None):
     """Attention of each token over its listed pages (kv_idx [slots, Hkv, T, W], kv_cnt [slots, Hkv,
     T], int32). Returns (out, lse, status)."""
-    query = _query(q, cache)
-    T, H = query[1], cache.k.shape[2]
+    p = cache._plan or cache._make_plan()
+    query = _query(q, p)
+    T = query[1]
     if not isinstance(kv_idx, torch.Tensor) or kv_idx.dim() != 4:
         _bad("kv_idx must be [slots, Hkv, T, W]")
     W = kv_idx.shape[3]
-    i = _tensor("kv_idx", kv_idx, (cache.slots, H, T, W), torch.int32, cache.device)
-    c = _tensor("kv_cnt", kv_cnt, (cache.slots, H, T), torch.int32, cache.device)
-    return _attend("bsa_attend_pages", q, query, cache, (i, c, W), q_len, layer, scale, out, lse, stream)
+    i = _tensor("kv_idx", kv_idx, (p.slots, p.Hkv, T, W), torch.int32, p.device)
+    c = _tensor("kv_cnt", kv_cnt, (p.slots, p.Hkv, T), torch.int32, p.device)
+    s = _stream(p, stream)
+    if s is None:
+        return _elsewhere(p, stream, attend_pages, q, cache, kv_idx, kv_cnt, q_len=q_len, layer=layer,
+                          scale=scale, out=out, lse=lse)
+    return _attend(lib().bsa_attend_pages, q, query, cache, p, (i, c, W), q_len, layer, scale, out, lse, s)
 
 
 def select_pages(q: torch.Tensor, cache: PagedCache, cfg: PageSelectConfig, *, q_len=None, layer: int = 0,
@@ -356,29 +387,28 @@ def select_pages(q: torch.Tensor, cache: PagedCache, cfg: PageSelectConfig, *, q
     """Pages for each token by the K-min/K-max bound of their keys. Returns a dict: kv_idx [slots,
     Hkv, T, k], kv_cnt [slots, Hkv, T], scores [slots, Hkv, T, max_pages] (None unless
     want_scores), dev_status."""
-    Hq, T, qp = _query(q, cache)
-    H = cache.k.shape[2]
-    ql = _qlen(cache, q_len)
-    _, _, b = cache._layer(layer)
+    p = cache._plan or cache._make_plan()
+    Hq, T, qp = _query(q, p)
+    ql = _qlen(cache, p, q_len)
+    b = cache._layer(p, layer)[2]
     if b is None:
         _bad("the cache has no bounds")
-    shape = cache.shape()
-    params = PageSelectParams(cfg.k, cfg.n_first, cfg.n_last)
-    dev = cache.device
-    with _On(dev, stream) as s:
-        nb = cache.workspace_bytes("select_pages", Hq, T)
-        if not 1 <= cfg.k <= cache.max_pages:
-            _bad("k must be 1..max_pages")
-        r = dict(kv_idx=cache.refs.new_empty(cache.slots, H, T, cfg.k),
-                 kv_cnt=cache.refs.new_empty(cache.slots, H, T),
-                 scores=(torch.empty(cache.slots, H, T, cache.max_pages, dtype=torch.float32, device=dev)
-                         if want_scores else None),
-                 dev_status=_status(cache.refs))
-        ws = None if want_scores else cache._scratch(nb)
-        _check(lib().bsa_select_pages(shape, ctypes.byref(params), cache.slots, cache.max_pages,
-                                      Hq, T, qp, b, cache.page_table.data_ptr(), cache.seq_len.data_ptr(), ql,
-                                      r["kv_idx"].data_ptr(), r["kv_cnt"].data_ptr(),
-                                      r["scores"].data_ptr() if want_scores else None,
-                                      r["dev_status"].data_ptr(), ws.data_ptr() if ws is not None else None,
-                                      nb, s))
-    return r
+    if not 1 <= cfg.k <= p.max_pages:
+        _bad("k must be 1..max_pages")
+    s = _stream(p, stream)
+    if s is None:
+        return _elsewhere(p, stream, select_pages, q, cache, cfg, q_len=q_len, layer=layer, want_scores=want_scores)
+    nb = cache.workspace_bytes("select_pages", Hq, T)
+    refs = cache.refs
+    idx, cnt, st = refs.new_empty(p.slots, p.Hkv, T, cfg.k), refs.new_empty(p.slots, p.Hkv, T), refs.new_empty(1)
+    scores = ws = None
+    if want_scores:
+        scores = refs.new_empty((p.slots, p.Hkv, T, p.max_pages), dtype=torch.float32)
+    else:
+        ws = refs.new_empty((nb + 3) // 4)
+    _check(lib().bsa_select_pages(p.shape, ctypes.byref(PageSelectParams(cfg.k, cfg.n_first, cfg.n_last)), p.slots,
+                                  p.max_pages, Hq, T, qp, b, cache.page_table.data_ptr(),
+                                  cache.seq_len.data_ptr(), ql, idx.data_ptr(), cnt.data_ptr(),
+                                  scores.data_ptr() if want_scores else None, st.data_ptr(),
+                                  None if want_scores else ws.data_ptr(), nb, s))
+    return dict(kv_idx=idx, kv_cnt=cnt, scores=scores, dev_status=st)
