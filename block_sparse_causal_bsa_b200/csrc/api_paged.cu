@@ -286,7 +286,8 @@ bsa_status bsa_attend_pages(const bsa_cache_shape* s, int slots, int max_pages, 
   if (st == BSA_OK) st = check_heads(s, slots, Hq, T);
   if (st != BSA_OK) return st;
   if (!kv_idx || !kv_cnt) return fail(BSA_ERR_INVALID_ARG, "NULL kv_idx or kv_cnt");
-  if (W < 1 || W > max_pages) return fail(BSA_ERR_INVALID_ARG, "W must be 1..max_pages");
+  if (W < 1) return fail(BSA_ERR_INVALID_ARG, "W must be >= 1");
+  if (W > bsa::kMaxTablePages) return fail(BSA_ERR_UNSUPPORTED, "W must be at most %d", bsa::kMaxTablePages);
   return attend(s, slots, max_pages, Hq, T, q, k, v, page_table, seq_len, q_len, nullptr, kv_idx, kv_cnt, W,
                 scale, out, lse, dev_status, ws, ws_bytes, stream);
 }
@@ -304,8 +305,9 @@ bsa_status bsa_select_pages(const bsa_cache_shape* s, const bsa_page_select_para
   if (st == BSA_OK) st = check_heads(s, slots, Hq, T);
   if (st != BSA_OK) return st;
   if (!p) return fail(BSA_ERR_INVALID_ARG, "params is NULL");
-  if (p->n_first < 0 || p->n_last < 1 || p->k > max_pages || p->n_first > p->k || p->n_last > p->k - p->n_first)
-    return fail(BSA_ERR_INVALID_ARG, "need n_first >= 0, n_last >= 1, n_first + n_last <= k <= max_pages");
+  if (p->n_first < 0 || p->n_last < 1 || p->n_first > p->k || p->n_last > p->k - p->n_first)
+    return fail(BSA_ERR_INVALID_ARG, "need n_first >= 0, n_last >= 1, n_first + n_last <= k");
+  if (p->k > bsa::kMaxTablePages) return fail(BSA_ERR_UNSUPPORTED, "k must be at most %d", bsa::kMaxTablePages);
   if (!q || !bounds || !page_table || !seq_len || !kv_idx || !kv_cnt || !dev_status)
     return fail(BSA_ERR_INVALID_ARG, "NULL q, bounds, page_table, seq_len, kv_idx, kv_cnt or dev_status");
   if (!aligned(q, 16) || !aligned(bounds, 16)) return fail(BSA_ERR_INVALID_ARG, "q and bounds need 16-byte alignment");

@@ -450,7 +450,7 @@ size_t bsa_attend_paged_workspace_bytes(const bsa_cache_shape* shape, int slots,
  *   kv_cnt [slots,Hkv,T] int32. Rows of tokens t >= q_len get -1 and 0.
  *   scores [slots,Hkv,T,max_pages] fp32 or NULL: s(t,j) for every j <= J, -inf beyond and for tokens
  *          t >= q_len. NULL: they pass through the workspace.
- *   n_first >= 0, n_last >= 1, n_first + n_last <= k <= max_pages.
+ *   n_first >= 0, n_last >= 1, n_first + n_last <= k <= 32768 (k may exceed the pages there are).
  *   A ranked page whose score is not finite is reported as BSA_DEV_BAD_SCORE and ranks last (a score
  *   with an infinite or NaN operand is NaN), as does a page number that the table does not hold
  *   (BSA_DEV_BAD_INDEX).
@@ -469,7 +469,7 @@ bsa_status bsa_select_pages(const bsa_cache_shape* shape, const bsa_page_select_
 /* Attention of each token over the listed pages: kv_idx [slots,Hkv,T,W], kv_cnt [slots,Hkv,T] as
  * written by bsa_select_pages (or any other lists; each page listed once). Token t sees the
  * positions <= base + t of its pages. An entry outside 0..J is skipped and a count outside 0..W
- * clamped (BSA_DEV_BAD_INDEX). W >= 1. Other arguments and results as bsa_attend_tree. */
+ * clamped (BSA_DEV_BAD_INDEX). 1 <= W <= 32768. Other arguments and results as bsa_attend_tree. */
 bsa_status bsa_attend_pages(const bsa_cache_shape* shape, int slots, int max_pages, int Hq, int T,
                             const void* q, const void* k_pages, const void* v_pages,
                             const int32_t* page_table, const int32_t* seq_len, const int32_t* q_len,

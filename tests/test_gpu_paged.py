@@ -271,6 +271,21 @@ def test_select_budgets_chain(k, n_first, n_last):
                 cfg=paged.PageSelectConfig(k, n_first, n_last))
 
 
+def test_budget_beyond_the_table():
+    """k past the pages that the table has room for: lists of every page, padded."""
+    lens, page = [100, 16, 1], 16
+    cache = make_cache(82, lens=lens, max_pages=7, page=page, Hkv=2, d=64)
+    q = torch.randn(3, 4, 1, 64, generator=torch.Generator().manual_seed(83)).to(torch.bfloat16).cuda()
+    sel = paged.select_pages(q, cache, paged.PageSelectConfig(50, 1, 1))
+    for b, n in enumerate(lens):
+        m = -(-n // page)
+        assert sel["kv_idx"][b, 1, 0].tolist() == list(range(m)) + [-1] * (50 - m)
+    out, lse, st = paged.attend_pages(q, cache, sel["kv_idx"], sel["kv_cnt"])
+    full, lsef, st2 = paged.attend_tree(q, cache)
+    assert int(st) == 0 and int(st2) == 0
+    assert torch.equal(out, full) and torch.allclose(lse, lsef, atol=1e-5)
+
+
 def test_select_ties_go_to_the_lower_page():
     """Copies of pages, and q = 0 (every score equal): the lowest indexes win."""
     lens, page = [64 * 16], 16
