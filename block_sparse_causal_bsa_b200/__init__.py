@@ -1,7 +1,7 @@
 """Block-sparse causal attention for NVIDIA B200 (sm_100a).
 
 The compute lives in libbsa.so (C ABI: include/bsa.h); ``binding`` is its
-ctypes wrapper, ``synthetic`` the seeded input generators.
+ctypes wrapper, ``paged`` the calls of the paged cache, ``synthetic`` the seeded input generators.
 """
 from .binding import (  # noqa: F401
     BsaError, SelectConfig, Shape, SelectParams, DecodeShape, DecodeParams, ScoreParams,
@@ -10,3 +10,4 @@ from .binding import (  # noqa: F401
     bsa_decode_list, bsa_select_noalloc, bsa_selftest_wait, score, select, attend, attend_vs,
     decode, prefill, lib,
 )
+from . import paged  # noqa: F401

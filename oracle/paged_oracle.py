@@ -1,7 +1,7 @@
 """CPU oracle of the paged-cache operators: plain, slow, fp64 and Python integers.
 
-TEST INFRASTRUCTURE, as ``bsa_oracle``: only the tests import it, and it imports nothing from
-the product. Pools are numpy fp64 arrays (the 16-bit values widened exactly): K, V
+TEST INFRASTRUCTURE, as ``bsa_oracle``: only the tests and the package smoke check import it,
+and it imports nothing from the product. Pools are numpy fp64 arrays (the 16-bit values widened exactly): K, V
 [n_pages, Hkv, page, d], bounds [n_pages, Hkv, 2, d]; tables are lists of lists of page numbers.
 """
 from __future__ import annotations
