@@ -28,12 +28,14 @@ struct CacheGeom {
 __host__ __device__ inline bool query_span(const CacheGeom& g, int b, int& base, int& ql) {
   const int len = g.seq_len[b];
   ql = g.q_len ? g.q_len[b] : g.T;
-  base = len - ql;
+  base = 0;
   if (ql == 0) return true;
-  if (ql < 0 || ql > g.T || base < 0 || (long long)len > (long long)g.max_pages * g.page) {
+  // (each compared by itself: a difference of wild lengths could overflow to one that fits)
+  if (ql < 0 || ql > g.T || len < ql || (long long)len > (long long)g.max_pages * g.page) {
     ql = 0;
     return false;
   }
+  base = len - ql;
   return true;
 }
 
