@@ -114,6 +114,13 @@ class PagedCache:
             object.__setattr__(self, "_plan", None)
             object.__setattr__(self, "_bytes", {})
 
+    def __getstate__(self):                      # copies and pickles hold the tensors alone
+        return {f.name: getattr(self, f.name) for f in dataclasses.fields(self)}
+
+    def __setstate__(self, state):
+        for name, value in state.items():
+            setattr(self, name, value)
+
     def shape(self):
         """The C shape (by reference), kept until a tensor of the cache is replaced."""
         return (self._plan or self._make_plan()).shape
@@ -135,7 +142,6 @@ class PagedCache:
                 _bad(lib().bsa_last_error().decode(), BSA_ERR_UNSUPPORTED)
             self._bytes[(call, Hq, T)] = n
         return n
-
 
     def _layer(self, p, layer: int):
         if not 0 <= layer < p.layers:

@@ -1,5 +1,7 @@
 """Refusals of the paged-cache calls that the host makes: nothing here reaches a kernel."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -134,3 +136,17 @@ def test_wrappers_refuse_wrong_tensors():
     # right in every other way, but there is no kernel for the CPU
     with pytest.raises(bb.BsaError, match="GPU"):
         paged.attend_tree(q, c)
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda c: pickle.loads(pickle.dumps(c))])
+def test_caches_can_be_copied_and_pickled(how):
+    c = paged.PagedCache.create(layers=1, n_pages=4, Hkv=1, page=16, d=64, slots=2, max_pages=2, device="cpu")
+    c.refs[1] = 3
+    n = c.workspace_bytes("attend_paged", 2, 1)
+    other = how(c)
+    assert torch.equal(other.refs, c.refs) and other.k.shape == c.k.shape
+    other.page_table = torch.full((3, 2), -1, dtype=torch.int32)       # what is derived follows its own tensors
+    other.seq_len = torch.zeros(3, dtype=torch.int32)
+    assert other.workspace_bytes("attend_paged", 2, 1) == n and other.slots == 3 and c.slots == 2
+    other.shape()
+    c.shape()
