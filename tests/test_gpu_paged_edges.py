@@ -66,3 +66,99 @@ def test_wild_lengths_are_left_out(T, wild_len, wild_ql):
     assert int(st) == bb.BSA_DEV_BAD_INDEX
     assert cache.seq_len.tolist() == [70] + wild_len
     assert torch.equal(cache.page_table, table) and torch.equal(cache.refs, refs)
+
+
+@pytest.mark.parametrize("T", [63, 64, 65, 200, 1000, 1024])
+def test_masks_of_long_trees(T):
+    rng = random.Random(T)
+    par = [[t - 1 for t in range(T)],                                          # a chain
+           [-1 if t == 0 else rng.randint(max(0, t - 90), t - 1) for t in range(T)],
+           [-1 if t < 3 else rng.randint(0, t - 1) for t in range(T)]]
+    ql = [T, T, T - 17]
+    mask, st = paged.tree_mask(_i32(par), q_len=_i32(ql))
+    assert int(st) == 0
+    want = words(np.stack([O.ancestors(p) for p in par]))
+    for b in range(3):
+        assert torch.equal(mask[b, :ql[b]].cpu(), want[b, :ql[b]]) and (mask[b, ql[b]:] == 0).all()
+
+
+def _check_slot(go, gl, qn, cache, b, n, ql, see, dtype, p_bits):
+    """Rows [Hq, ql, d] of a slot against the formula in 64 bits."""
+    Hkv, page, d = cache.k.shape[2:]
+    pages = cache.page_table[b, :-(-n // page)].cpu().long()
+    G = qn.shape[0] // Hkv
+    vis = np.ones((ql, n), bool)
+    vis[:, n - ql:] = see
+    for h in range(Hkv):
+        kr, vr = (f8(x[0, pages.to(x.device), h].reshape(-1, d)[:n]) for x in (cache.k, cache.v))
+        qh = qn[h * G:(h + 1) * G, :ql].reshape(G * ql, d)
+        ro, rl = O.softmax_rows(qh, kr, vr, np.tile(vis, (G, 1)), scale_of(d))
+        km, vm = np.abs(kr).max(), np.abs(vr).max()
+        check(go[h * G:(h + 1) * G, :ql].reshape(-1, d), ro,
+              out_tolerance(ro, qh, km, vm, d, scale_of(d), dtype, p_bits), (b, h))
+        check(gl[h * G:(h + 1) * G, :ql].reshape(-1), rl, lse_tolerance(rl, qh, km, d, scale_of(d), n), (b, h))
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,page,d,tree", [(1024, 2, 1, 128, 128, False), (1000, 3, 1, 16, 64, True),
+                                                  (257, 16, 1, 64, 128, True), (300, 1, 1, 32, 64, False)])
+def test_long_chunks_and_trees(T, Hq, Hkv, page, d, tree):
+    """Several row tiles per item of one KV head, up to sixteen mask words."""
+    rng = random.Random(T)
+    qls = [T, T - 1, 129]
+    lens = [T, T + 777, 140]
+    cache = make_cache(5, lens=lens, max_pages=-(-max(lens) // page), page=page, Hkv=Hkv, d=d,
+                       garbage=float("nan"))
+    par = [[-1 if t == 0 else rng.randint(max(0, t - 70), t - 1) for t in range(T)] for _ in lens]
+    see = np.stack([O.ancestors(p) for p in par]) if tree else np.broadcast_to(np.tril(np.ones((T, T), bool)), (3, T, T))
+    q = _randn(6, 3, Hq, T, d)
+    out, lse, st = paged.attend_tree(q, cache, mask=words(see).cuda() if tree else None, q_len=_i32(qls))
+    assert int(st) == 0
+    for b, (n, ql) in enumerate(zip(lens, qls)):
+        _check_slot(f8(out[b]), f8(lse[b]), f8(q[b]), cache, b, n, ql, see[b, :ql, :ql], "bf16", 8)
+        assert (out[b, :, ql:] == 0).all() and torch.isneginf(lse[b, :, ql:]).all()
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 4, 2), (12, 4, 2)])
+def test_a_table_of_mostly_idle_slots(T, Hq, Hkv):
+    slots, page, d = 4096, 16, 64
+    lens, qls = [0] * slots, [0] * slots
+    for s, n in [(0, 33), (31, 70), (32, T), (1999, 500), (4095, 129)]:
+        lens[s], qls[s] = n, T
+    lens[77] = 64                                          # rows, but no token in the call
+    cache = make_cache(9, lens=lens, max_pages=32, page=page, Hkv=Hkv, d=d)
+    q = _randn(10, slots, Hq, T, d)
+    out, lse, st = paged.attend_tree(q, cache, q_len=_i32(qls))
+    sel = paged.select_pages(q, cache, paged.PageSelectConfig(32, 1, 1), q_len=_i32(qls))
+    out2, lse2, st2 = paged.attend_pages(q, cache, sel["kv_idx"], sel["kv_cnt"], q_len=_i32(qls))
+    assert int(st) == int(st2) == int(sel["dev_status"]) == 0
+    see = np.tril(np.ones((T, T), bool))
+    for s in range(slots):
+        if qls[s]:
+            for o, l, p_bits in ((out, lse, 16 if Hq // Hkv * T <= 16 else 8), (out2, lse2, 16)):
+                _check_slot(f8(o[s]), f8(l[s]), f8(q[s]), cache, s, lens[s], T, see, "bf16", p_bits)
+    idle = torch.tensor([n == 0 for n in qls])
+    for o, l in ((out, lse), (out2, lse2)):
+        assert (o.cpu()[idle] == 0).all() and torch.isneginf(l.cpu()[idle]).all()
+    # nobody takes part
+    none = _i32([0] * slots)
+    out, lse, st = paged.attend_tree(q, cache, q_len=none)
+    assert int(st) == 0 and (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_a_list_as_long_as_it_may_be():
+    """32768 entries for a table of 40 pages: the row's count says how many of them are read."""
+    page, d = 16, 64
+    cache = make_cache(11, lens=[600, 9], max_pages=40, page=page, Hkv=1, d=d)
+    W = 32768
+    idx = torch.full((2, 1, 1, W), 12345, dtype=torch.int32, device="cuda")
+    idx[0, 0, 0, :38] = torch.randperm(38, generator=torch.Generator().manual_seed(1)).int().cuda()
+    idx[1, 0, 0, 0] = 0
+    cnt = _i32([38, 1]).view(2, 1, 1)
+    q = _randn(12, 2, 3, 1, d)
+    out, lse, st = paged.attend_pages(q, cache, idx, cnt)
+    assert int(st) == 0
+    for b, n in enumerate([600, 9]):
+        _check_slot(f8(out[b]), f8(lse[b]), f8(q[b]), cache, b, n, 1, np.ones((1, 1), bool), "bf16", 16)
+    # all of them the same page past the end, the count as large as it may be: all skipped
+    out, lse, st = paged.attend_pages(q, cache, torch.full_like(idx, 39), _i32([W, W]).view(2, 1, 1))
+    assert int(st) == bb.BSA_DEV_BAD_INDEX and (out == 0).all() and torch.isneginf(lse).all()
