@@ -398,8 +398,9 @@ bsa_status bsa_pages_copy(const bsa_cache_shape* shape, void* k_pages, void* v_p
 
 /* Append: writes k_new, v_new [slots,Hkv,T,d] to the positions of the call's tokens (seq_len
  * already counts them: resize comes first) and extends the bounds (NULL: none) of the pages they
- * fall in; a page whose first row is among them starts afresh. No two slots may append to one
- * page (resize gives each its own). */
+ * fall in; a page whose first row is among them starts afresh. A page that is written must not
+ * be held by another slot, which would see the change (a resize that grows the slot gives it
+ * a page of its own). */
 bsa_status bsa_cache_append(const bsa_cache_shape* shape, int slots, int max_pages, int T,
                             const void* k_new, const void* v_new, void* k_pages, void* v_pages,
                             void* bounds, const int32_t* page_table, const int32_t* seq_len,
@@ -409,7 +410,9 @@ bsa_status bsa_cache_append(const bsa_cache_shape* shape, int slots, int max_pag
  * ascending, in 0..q_len[s]-1): row base + keep[s][i] moves to base + i, in K and V, and the bounds
  * (NULL: none) of the pages from that of base to that of base + n_keep[s] - 1 are recomputed over the
  * rows kept. Lengths are not changed: resize to base + n_keep[s] afterwards (it frees the pages
- * behind). A slot with a bad list is left as it was (BSA_DEV_BAD_INDEX). */
+ * behind). As for bsa_cache_append, no other slot may hold the pages written: fork after this
+ * call, not between the append and it. A slot with a bad list is left as it was
+ * (BSA_DEV_BAD_INDEX). */
 bsa_status bsa_cache_compact(const bsa_cache_shape* shape, int slots, int max_pages, int T,
                              const int32_t* keep, const int32_t* n_keep, void* k_pages, void* v_pages,
                              void* bounds, const int32_t* page_table, const int32_t* seq_len,
