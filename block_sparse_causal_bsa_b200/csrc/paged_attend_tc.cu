@@ -90,6 +90,9 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
 // the four softmax warps of a group; both groups
 __device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
 __device__ __forceinline__ void both_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+// Turns at the exponentials: two warps, one of each group, that share a scheduler.
+__device__ __forceinline__ void turn_wait(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void turn_pass(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
 
 // Keys of the tile that starts dj positions after the slot's first token (dj may be negative) that
 // token t sees: bit i for key i.
@@ -384,6 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&b.q_full);
     };
+    const int my_turn = 4 + 4 * g + quarter, other_turn = 4 + 4 * (1 - g) + quarter;
+    if (g == 1) turn_pass(other_turn);
     int n = 0, seg = 0, j = 0;                           // j: tiles of this group
     bool ok = true;
     Row me{};
@@ -400,13 +405,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
       const int r0 = me.r0, rows = me.rows, t = me.t, r = r0 + rt;
       const bool row_ok = me.ok;
       const bool live = quarter * 32 < rows;             // the warp has rows
+      const bool turns = !share;                         // both groups: every tile
       const size_t grow = me.row;
       float m_used = -INFINITY, l = 0.f;
       bool first = true;                                 // no tile of the group in this segment yet
       for (int tile = ta; tile < tb; ++tile, ++n) {
         if (share && (n & 1) != g) continue;
         if (ok) ok = warp_all(tc::mbar_wait(&b.s_full[j % 2], (j / 2) & 1, abort_flag, status));
-        if (!ok) continue;
+        if (!ok) {
+          if (turns) {
+            turn_wait(my_turn);
+            turn_pass(other_turn);
+          }
+          continue;
+        }
         tc::tc_fence_after();
         const int pos0 = tile * kTileKeys;
         const uint64_t vm = c.vmask[n % kMaskRing];
@@ -415,7 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
           // mend the V tile: rows that are no keys become 0, non-finite drafted values are taken out
           // (by both groups, alike, where both use the tile)
           ok = warp_all(tc::mbar_wait(&c.v_full[n % NS], (n / NS) & 1, abort_flag, status));
-          if (!ok) continue;
+          if (!ok) {
+            if (turns) {
+              turn_wait(my_turn);
+              turn_pass(other_turn);
+            }
+            continue;
+          }
           const int row = tid / 2;
           const bool key = (vm >> row) & 1;
           if (!key || (drafts && pos0 + row >= it.base)) {
@@ -471,7 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
             alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - m_tile);
             m_used = m_tile;
           }
-          const float z = kShift - ((m_used == -INFINITY) ? 0.f : m_used);
+          float z = kShift - ((m_used == -INFINITY) ? 0.f : m_used);
+          if (turns) {
+            turn_wait(my_turn);
+            asm volatile("" : "+f"(z));
+          }
           float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
@@ -485,6 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
             add2(sum2, sum3, p2, p3);
           }
           l = l * alpha + ((sum0 + sum1) + (sum2 + sum3));
+          if (turns) turn_pass(other_turn);
+        } else if (turns) {
+          turn_wait(my_turn);
+          turn_pass(other_turn);
         }
         if (j > 0) {
           // the previous value product has landed: O may be rescaled, and the arrival below is
@@ -603,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
       x = xe;
       it = nx;
     }
+    if (g == 0) turn_wait(my_turn);
   }
 
   // ---------------- teardown ----------------
