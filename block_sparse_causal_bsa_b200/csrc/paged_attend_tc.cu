@@ -87,6 +87,13 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
       "add.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
       : "+f"(a0), "+f"(a1) : "f"(b0), "f"(b1));
 }
+// x = x f + z, twice
+__device__ __forceinline__ void fma2(float& x0, float& x1, float f, float z) {
+  asm("{\n\t.reg .b64 ra, rb, rc;\n\t"
+      "mov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %2};\n\tmov.b64 rc, {%3, %3};\n\t"
+      "fma.rn.f32x2 ra, ra, rb, rc;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(x0), "+f"(x1) : "f"(f), "f"(z));
+}
 // the four softmax warps of a group; both groups
 __device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
 __device__ __forceinline__ void both_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
@@ -468,22 +475,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
 #pragma unroll
             for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(v[i]);
           }
-          float mx8[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) mx8[u] = -INFINITY;
           if (vm != ~0ull || drafts) {
             const uint64_t keep = vm & (drafts ? draft_window(a, it.b, t, pos0 - it.base) : ~0ull);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              s[i] = ((keep >> i) & 1ull) ? s[i] : -INFINITY;
-              mx8[i & 7] = fmaxf(mx8[i & 7], s[i]);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) mx8[i & 7] = fmaxf(mx8[i & 7], s[i]);
+            for (int i = 0; i < 64; ++i) s[i] = ((keep >> i) & 1ull) ? s[i] : -INFINITY;
           }
-          const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          float mx4[4];                                  // (three-operand maxima)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx4[u] = fmaxf(s[u], s[u + 4]);
+#pragma unroll
+          for (int i = 8; i < 64; i += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mx4[u] = fmaxf(fmaxf(mx4[u], s[i + u]), s[i + u + 4]);
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float m_tile = mx * scale_log2;
           if (m_tile > m_used + 8.0f) {                  // also taken when m_used is -inf
             alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - m_tile);
@@ -497,10 +501,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
           float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
-            const float p0 = ex2(fmaf(s[i], scale_log2, z));
-            const float p1 = ex2(fmaf(s[i + 1], scale_log2, z));
-            const float p2 = ex2(fmaf(s[i + 2], scale_log2, z));
-            const float p3 = ex2(fmaf(s[i + 3], scale_log2, z));
+            fma2(s[i], s[i + 1], scale_log2, z);
+            fma2(s[i + 2], s[i + 3], scale_log2, z);
+            const float p0 = ex2(s[i]), p1 = ex2(s[i + 1]), p2 = ex2(s[i + 2]), p3 = ex2(s[i + 3]);
             pk[i / 2] = pack_16<F16>(p0, p1);
             pk[i / 2 + 1] = pack_16<F16>(p2, p3);
             add2(sum0, sum1, p0, p1);
