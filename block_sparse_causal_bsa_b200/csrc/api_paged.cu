@@ -103,7 +103,7 @@ AttendWs attend_ws(const bsa_cache_shape& s, int Hq, int T, bool list, void* bas
   const int rows = (Hq / s.Hkv) * (list ? 1 : T);
   const bool tc = rows > bsa::kMaxMmaRows;
   const int rt = tc ? 256 : (rows <= 8 ? 8 : 16);
-  w.n_cta = std::min(bsa::sm_count(), bsa::kMaxPartsCtas);
+  w.n_cta = bsa::sm_count() * (tc ? 1 : bsa::kMmaSharesPerSm);
   w.n_arrived = (tc ? 2 : 1) * w.n_cta;
   w.tc = tc;
   const size_t slots = 2 * (size_t)w.n_cta;

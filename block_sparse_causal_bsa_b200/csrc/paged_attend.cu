@@ -5,19 +5,23 @@
 //
 // The rows of an item (at most RT = 8 or 16) meet every key of a long cache: 4 d RT flops for 4 d
 // bytes of K and V per key, so the kernel is bound by the HBM reads of the cache. What it does about
-// it: one CTA per SM streams its equal share of all key tiles (paged_work.cuh) through a ring of
+// it: a CTA streams its equal share of all key tiles (paged_work.cuh) through a ring of
 // TMA-fed stages that never drains between items, and the MMAs, exponentials and shared-memory
-// reads of a tile are spread over eight warps so that they stay under the time its bytes take.
+// reads of a tile are spread over four warps so that they stay under the time its bytes take. Two
+// CTAs share an SM: one streams while the other starts, writes a partial result or joins (one CTA of
+// twice the size: 16 sequences of 64k tokens 638 us, now 629, that is 6.8 TB/s; 12 drafted chains over
+// page lists 29 us, now 23). More, shorter shares than fit at once cost more starts than they even out
+// (16 x 8 lists of 64 pages: 55 us, with twice the shares 62).
 //
-// 320 threads:
-//   warps 0, 9 producers of K and of V (paged_feed.cuh)
-//   warps 1-8  two groups of four, taking tiles in turn; a warp owns 16 keys of its tiles and keeps its
-//              own online softmax over them (maximum m, sum l, unnormalised O):
+// 192 threads:
+//   warps 0, 5 producers of K and of V (paged_feed.cuh)
+//   warps 1-4  a warp owns 16 keys of every tile and keeps its own online softmax over them (maximum
+//              m, sum l, unnormalised O):
 //                S = K Q^T (A = K rows by ldmatrix, B = Q in registers), P = 2^(S scale log2 e - m),
 //                O^T += V^T P^T (A = V^T by ldmatrix.trans, B = P^T from S by movmatrix)
 //              P goes into the product as two 16-bit terms (value and rounding remainder), so O carries
 //              no rounding of P: the second MMA is free here, the tensor pipe idles anyway. At the end of
-//              a segment the eight states are joined in shared memory.
+//              a segment the four states are joined in shared memory.
 // For fp16, weights are scaled by 2^14: fp16's smallest value is 2^-24, and many small weights
 // would be lost below it.
 // Rows that are no keys (the tail of the last page, missing pages) have their S masked and their
@@ -33,7 +37,7 @@ namespace bsa {
 
 namespace {
 
-constexpr int kWarps = 8;                       // compute warps
+constexpr int kWarps = 4;                       // compute warps
 constexpr int kThreads = 32 * (kWarps + 2);
 
 __device__ __forceinline__ float ex2(float x) {
@@ -69,8 +73,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// the eight compute warps
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// the compute warps
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 template <int D, int RT>
 struct Cfg {
@@ -78,7 +82,9 @@ struct Cfg {
   static constexpr uint32_t kHalf = kTileKeys * 128;          // 64 rows x 128 bytes
   static constexpr uint32_t kTile = kHalves * kHalf;          // K or V of a tile
   static constexpr uint32_t kStage = 2 * kTile;
-  static constexpr int kStages = D == 128 ? (RT == 8 ? 6 : 5) : 8;
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kPasses = D * RT > 1024 ? 2 : 1;       // of the join of the warps' states
+  static constexpr int kDP = D / kPasses;                     // channels of a pass
 };
 
 // Column of channel d in row r of a dumped output: the rows 2 tig of a fragment's store fall eight
@@ -95,13 +101,13 @@ struct __align__(16) Ctrl {
   int last;                                     // this CTA joins the item's parts
   float m[kWarps][RT], l[kWarps][RT];
   union {
-    alignas(16) float o[kWarps][RT][D];      // the warps' unnormalised outputs
-    float2 ml[kWarps * RT * D / 2];             // maxima and sums of an item's parts
+    alignas(16) float o[kWarps][RT][Cfg<D, RT>::kDP];      // the warps' unnormalised outputs
+    float2 ml[kWarps * RT * Cfg<D, RT>::kDP / 2];             // maxima and sums of an item's parts
   };
 };
 
 template <int D, int RT>
-constexpr size_t smem_bytes() { return 1024 + Cfg<D, RT>::kStages * Cfg<D, RT>::kStage + sizeof(Ctrl<D, RT>); }
+constexpr size_t smem_bytes() { return Cfg<D, RT>::kStages * Cfg<D, RT>::kStage + sizeof(Ctrl<D, RT>); }
 
 // Four values of a row, final: normalised, rounded and stored, then the non-finite drafted values.
 template <int D, bool F16, bool LIST>
@@ -125,77 +131,101 @@ __device__ __forceinline__ void add4(float4& acc, const float4& v, float f) {
   acc.w = fmaf(v.w, f, acc.w);
 }
 
-// Joins the parts of an item, the 256 threads of the compute warps: four values of a row each, the
-// first reads of the parts' outputs on their way with those of their maxima and sums.
+// Joins the parts of an item, the threads of the compute warps: four values of a row at a time. Parts come in
+// chunks whose maxima and sums fit in shared memory (one chunk nearly always); the first reads of a chunk's
+// outputs are on their way with those of its maxima and sums.
 template <int D, int RT, bool F16, bool LIST>
 __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const Parts<LIST, RT>& parts,
                                        Ctrl<D, RT>& c, int tid, bool ok) {
   constexpr int kU = 8;                          // reads in flight
+  constexpr int kThr = 32 * kWarps;
+  constexpr int kNI = RT * (D / 4) / kThr;       // quads of values per thread
+  constexpr int kChunk = sizeof(c.ml) / (RT * sizeof(float2));
   // (copies: behind the ordered reads below, what the references name would be read again each time)
   const float* const part_o = a.part_o;
   const float2* const part_ml = reinterpret_cast<const float2*>(a.part_ml);
   const int32_t* const part_flag = a.part_flag;
   const Parts<LIST, RT> pt = parts;
-  const int np = pt.n, rows = it.rows;
-  static_assert(sizeof(c.ml) >= kMaxPartsCtas * RT * sizeof(float2), "room for every part");
-  for (int i = tid; i < np * RT; i += 32 * kWarps)
-    c.ml[i] = read_l2(part_ml + pt.slot(i / RT) * RT + i % RT);
+  const int np = pt.n, quads = it.rows * (D / 4);
   if (!LIST)
-    for (int i = tid; i < np; i += 32 * kWarps)
+    for (int i = tid; i < np; i += kThr)
       if (read_l2(part_flag + pt.slot(i))) atomicOr(&c.last, 2);
-  float4 v[kU];
-  auto read = [&](int i, int p0) {
-    const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
+  float4 acc[kNI];
+  float mx[kNI], ls[kNI];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p0 + u < np && r < rows)
-        v[u] = read_l2(reinterpret_cast<const float4*>(part_o + (pt.slot(p0 + u) * RT + r) * D + d4));
-    }
-  };
-  if (tid < RT * (D / 4)) read(tid, 0);
-  compute_sync();
-  for (int i = tid; i < RT * (D / 4); i += 32 * kWarps) {
-    const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
-    if (i != tid) read(i, 0);
-    float mx = -INFINITY, ls = 0.f;
-    for (int p = 0; p < np; ++p) mx = fmaxf(mx, c.ml[p * RT + r].x);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < np; p0 += kU) {
-      if (p0) read(i, p0);
+  for (int k = 0; k < kNI; ++k) {
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    mx[k] = -INFINITY;
+    ls[k] = 0.f;
+  }
+  for (int c0 = 0; c0 < np; c0 += kChunk) {
+    const int nc = min(np - c0, kChunk);
+    if (c0) compute_sync();                      // the chunk before has been used
+    for (int i = tid; i < nc * RT; i += kThr) c.ml[i] = read_l2(part_ml + pt.slot(c0 + i / RT) * RT + i % RT);
+    float4 v[kU];
+    auto read = [&](int i, int p0) {
+      const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        if (p0 + u < np) {
-          const float2 ml = c.ml[(p0 + u) * RT + r];
-          const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
-          ls += ml.y * f;
-          add4(acc, v[u], f);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p0 + u < nc && i < quads)
+          v[u] = read_l2(reinterpret_cast<const float4*>(part_o + (pt.slot(c0 + p0 + u) * RT + r) * D + d4));
+      }
+    };
+    read(tid, 0);
+    compute_sync();
+#pragma unroll
+    for (int k = 0; k < kNI; ++k) {
+      const int i = tid + k * kThr, r = i / (D / 4);
+      if (i >= quads) continue;
+      if (k) read(i, 0);
+      float m = mx[k];
+      for (int p = 0; p < nc; ++p) m = fmaxf(m, c.ml[p * RT + r].x);
+      if (c0) {
+        const float f = mx[k] == -INFINITY ? 0.f : ex2(mx[k] - m);
+        ls[k] *= f;
+        acc[k] = make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
+      }
+      mx[k] = m;
+      for (int p0 = 0; p0 < nc; p0 += kU) {
+        if (p0) read(i, p0);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          if (p0 + u < nc) {
+            const float2 ml = c.ml[(p0 + u) * RT + r];
+            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+            ls[k] += ml.y * f;
+            add4(acc[k], v[u], f);
+          }
         }
       }
     }
-    if (ok && r < it.rows) store_row4<D, F16, LIST>(a, it, r, d4, acc, mx, ls, c.last & 2);
+  }
+#pragma unroll
+  for (int k = 0; k < kNI; ++k) {
+    const int i = tid + k * kThr;
+    if (ok && i < quads) store_row4<D, F16, LIST>(a, it, i / (D / 4), (i % (D / 4)) * 4, acc[k], mx[k], ls[k], c.last & 2);
   }
 }
 
 }  // namespace
 
 template <int D, int RT, bool F16, bool LIST>
-__global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
+__global__ void __launch_bounds__(kThreads, 2) paged_attend_kernel(
     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
     const __grid_constant__ PagedArgs a) {
   using C = Cfg<D, RT>;
   constexpr int NT = RT / 8;                    // MMA column tiles of the rows
   constexpr int DM = D / 16;                    // MMA row tiles of the head dim
   constexpr float kShift = F16 ? 14.f : 0.f;      // (store_row4 takes it back)
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];   // (the kernel has no other shared memory)
   Ctrl<D, RT>& c = *reinterpret_cast<Ctrl<D, RT>*>(sm + C::kStages * C::kStage);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       tc::mbar_init(&c.full[s], 2);             // both producers
-      tc::mbar_init(&c.empty[s], kWarps / 2);
+      tc::mbar_init(&c.empty[s], kWarps);
     }
     c.abort_flag = 0;
     c.status = 0;
@@ -218,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
     issued = feed_share<LIST, RT, D, C::kStages, C::kStages>(a, w, x0, x1, f, abort_flag, &c.status);
   } else {
     // ---------------- compute ----------------
-    const int cw = warp - 1, group = cw / 4, kw = cw % 4;
+    const int kw = warp - 1;
     const int g8 = lane >> 2, tig = lane & 3;
     const uint32_t sStages = tc::smem_u32(sm);
     const uint32_t rowK = (uint32_t)(16 * kw + (lane & 7) + ((lane >> 3) & 1) * 8) * 128u;
@@ -271,7 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
         }
 
         for (int tile = ta; tile < tb; ++tile, ++n) {
-          if ((n & 1) != group) continue;
           const int s = n % C::kStages;
           if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&c.full[s], (n / C::kStages) & 1, abort_flag, &c.status));
           if (!ok) continue;                     // still joins the barriers below
@@ -396,50 +425,56 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(
           if (lane == 0) tc::mbar_arrive(&c.empty[s]);
         }
 
-        // ---- join the eight states: every warp leaves its own, then a thread adds up four values ----
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r = 8 * nt + 2 * tig + j;
-#pragma unroll
-            for (int dm = 0; dm < DM; ++dm) {
-              c.o[cw][r][dump_col(r, 16 * dm + g8)] = o[dm][nt][j];
-              c.o[cw][r][dump_col(r, 16 * dm + g8 + 8)] = o[dm][nt][2 + j];
-            }
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
-            if (g8 == 0) {
-              c.m[cw][r] = m[nt][j];
-              c.l[cw][r] = l[nt][j];
-            }
-          }
-        compute_sync();
+        // ---- join the warps' states: every warp leaves its own, then a thread adds up four values ----
         const int tid = threadIdx.x - 32;
         const bool whole = ta == 0 && tend == it.n_tiles;
-        const bool fixup = *(volatile int*)&c.flag[seg & 1];
         const size_t slot = 2 * (size_t)blockIdx.x + (ta == 0 ? 1 : 0);
-        for (int i = tid; i < RT * (D / 4); i += 32 * kWarps) {
-          const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
-          if (r >= it.rows) break;
-          float mw[kWarps], mx = -INFINITY, ls = 0.f;
+        int fixup = 0;
 #pragma unroll
-          for (int u = 0; u < kWarps; ++u) {
-            mw[u] = c.m[u][r];
-            mx = fmaxf(mx, mw[u]);
-          }
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int pass = 0; pass < C::kPasses; ++pass) {
+          if (pass) compute_sync();              // the pass before has been read
 #pragma unroll
-          for (int u = 0; u < kWarps; ++u) {
-            const float f = mw[u] == -INFINITY ? 0.f : ex2(mw[u] - mx);
-            ls += c.l[u][r] * f;
-            add4(v, *reinterpret_cast<const float4*>(&c.o[u][r][dump_col(r, d4)]), f);
-          }
-          if (whole) {
-            if (ok) store_row4<D, F16, LIST>(a, it, r, d4, v, mx, ls, fixup);
-          } else {
-            *reinterpret_cast<float4*>(a.part_o + (slot * RT + r) * D + d4) = v;
-            if (d4 == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * RT + r) * 2) = make_float2(mx, ls);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int r = 8 * nt + 2 * tig + j;
+#pragma unroll
+              for (int dm = 0; dm < DM / C::kPasses; ++dm) {
+                const int dd = pass * (DM / C::kPasses) + dm;
+                c.o[kw][r][dump_col(r, 16 * dm + g8)] = o[dd][nt][j];
+                c.o[kw][r][dump_col(r, 16 * dm + g8 + 8)] = o[dd][nt][2 + j];
+              }
+              if (pass) continue;
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
+              if (g8 == 0) {
+                c.m[kw][r] = m[nt][j];
+                c.l[kw][r] = l[nt][j];
+              }
+            }
+          compute_sync();
+          fixup = *(volatile int*)&c.flag[seg & 1];
+          for (int i = tid; i < it.rows * (C::kDP / 4); i += 32 * kWarps) {
+            const int r = i / (C::kDP / 4), dp = (i % (C::kDP / 4)) * 4, d4 = pass * C::kDP + dp;
+            float mw[kWarps], mx = -INFINITY, ls = 0.f;
+#pragma unroll
+            for (int u = 0; u < kWarps; ++u) {
+              mw[u] = c.m[u][r];
+              mx = fmaxf(mx, mw[u]);
+            }
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < kWarps; ++u) {
+              const float f = mw[u] == -INFINITY ? 0.f : ex2(mw[u] - mx);
+              ls += c.l[u][r] * f;
+              add4(v, *reinterpret_cast<const float4*>(&c.o[u][r][dump_col(r, dp)]), f);
+            }
+            if (whole) {
+              if (ok) store_row4<D, F16, LIST>(a, it, r, d4, v, mx, ls, fixup);
+            } else {
+              *reinterpret_cast<float4*>(a.part_o + (slot * RT + r) * D + d4) = v;
+              if (d4 == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * RT + r) * 2) = make_float2(mx, ls);
+            }
           }
         }
         if (!whole) {
@@ -526,7 +561,7 @@ static cudaError_t attend_t(const bsa_cache_shape& s, const PagedArgs& a, const 
     return cudaErrorInvalidValue;
   auto kern = paged_attend_kernel<D, RT, F16, LIST>;
   constexpr size_t smem = smem_bytes<D, RT>();
-  static_assert(smem <= 227 * 1024, "paged attend shared memory");
+  static_assert(smem <= 113 * 1024, "two CTAs per SM");
   static SmemSet set;
   cudaError_t e = allow_smem((const void*)kern, smem, set);
   if (e != cudaSuccess) return e;

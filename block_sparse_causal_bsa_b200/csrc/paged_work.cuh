@@ -359,8 +359,8 @@ cudaError_t launch_paged_attend_mma(const bsa_cache_shape& s, PagedArgs a, const
 cudaError_t launch_paged_attend_tc(const bsa_cache_shape& s, const PagedArgs& a, const void* k, const void* v,
                                    cudaStream_t st);
 
-// CTAs at most of the kernel on warp-level MMAs (its join keeps every part's maxima in shared memory).
-constexpr int kMaxPartsCtas = 256;
+// Shares per SM of the kernel on warp-level MMAs: the CTAs that fit.
+constexpr int kMmaSharesPerSm = 2;
 
 // Query rows per KV head up to which a call runs on warp-level MMAs.
 constexpr int kMaxMmaRows = 16;
