@@ -123,13 +123,14 @@ __device__ __forceinline__ float4* part4(float* part_o, size_t slot, int D, int 
   return reinterpret_cast<float4*>(part_o) + (slot * (D / 4) + d4) * RT + r;
 }
 // Joins the parts of the rows [r0, r0 + rows) of an item, channels 4 d0 .. 4 d1, one group: 128 / R
-// threads per row, R the rows rounded up to whole warps, each a run of channels; sixteen reads of 16
-// bytes in flight per thread.
+// threads per row, R the rows rounded up to whole warps, each a run of channels; four quads of channels of
+// three parts are read at once. (One user's eight drafts 20.8 -> 18.8 us against eight quads of two parts, of which
+// a short run has half; four parts take registers that the main loop then spills.)
 template <int D, bool F16>
 __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const Parts<false, RT>& parts, int r0,
                                        int rows, int d0, int d1, int flag_at, int tid, bool ok) {
   constexpr float kShift = F16 ? 7.f : 0.f;
-  constexpr int kU = 8;
+  constexpr int kU = 4, kP = 3;
   // (copies: behind the ordered reads below, what the references name would be read again each time)
   float* const part_o = a.part_o;
   const float2* const part_ml = reinterpret_cast<const float2*>(a.part_ml);
@@ -158,34 +159,27 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
 #pragma unroll
     for (int u = 0; u < kU; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     ls = 0.f;
-    for (int i = 0; i < np; i += 2) {
-      const int i1 = min(i + 1, np - 1);                       // (the odd last part counts once)
-      const size_t s0 = pt.slot(i), s1 = pt.slot(i1);
-      const float2 m0 = read_l2(ml_of(i)), m1 = read_l2(ml_of(i1));
-      float4 v[kU], w[kU];
+    for (int i = 0; i < np; i += kP) {
+      float2 ml[kP];
+      float4 v[kP][kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int d4 = min(dc + u, db - 1);
-        v[u] = read_l2(part4(part_o, s0, D, d4, r));
-        w[u] = read_l2(part4(part_o, s1, D, d4, r));
+      for (int k = 0; k < kP; ++k) {
+        const size_t at = pt.slot(min(i + k, np - 1));         // (past the last: a weight of 0 below)
+        ml[k] = read_l2(part_ml + at * RT + r);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) v[k][u] = read_l2(part4(part_o, at, D, min(dc + u, db - 1), r));
       }
-      const float f = m0.x == -INFINITY ? 0.f : ex2(m0.x - mx);
-      const float h = m1.x == -INFINITY || i1 == i ? 0.f : ex2(m1.x - mx);
-      ls += m0.y * f + m1.y * h;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        // (a weight of 0 must not meet what an empty part holds)
-        if (f != 0.f) {
-          acc[u].x = fmaf(v[u].x, f, acc[u].x);
-          acc[u].y = fmaf(v[u].y, f, acc[u].y);
-          acc[u].z = fmaf(v[u].z, f, acc[u].z);
-          acc[u].w = fmaf(v[u].w, f, acc[u].w);
-        }
-        if (h != 0.f) {
-          acc[u].x = fmaf(w[u].x, h, acc[u].x);
-          acc[u].y = fmaf(w[u].y, h, acc[u].y);
-          acc[u].z = fmaf(w[u].z, h, acc[u].z);
-          acc[u].w = fmaf(w[u].w, h, acc[u].w);
+      for (int k = 0; k < kP; ++k) {
+        const float f = ml[k].x == -INFINITY || i + k >= np ? 0.f : ex2(ml[k].x - mx);
+        if (f == 0.f) continue;                                // (must not meet what an empty part holds)
+        ls += ml[k].y * f;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          acc[u].x = fmaf(v[k][u].x, f, acc[u].x);
+          acc[u].y = fmaf(v[k][u].y, f, acc[u].y);
+          acc[u].z = fmaf(v[k][u].z, f, acc[u].z);
+          acc[u].w = fmaf(v[k][u].w, f, acc[u].w);
         }
       }
     }
