@@ -198,7 +198,8 @@ __device__ __forceinline__ int slot_of(const ResizeSmem& s, int slots, int i) {
 
 // Everything per slot sits in shared memory after one coalesced read, and every loop over pages runs
 // one page per thread, whatever slot it belongs to: the kernel is a chain of some ten barriers and
-// five memory latencies. (A warp per slot took 35 us for 504 slots.)
+// five memory latencies. (A warp per slot took 35 us to free 504 slots of up to 47 pages each, now 25: one SM's
+// rate of scattered atomics. Growing them takes 16.)
 __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(
     int slots, int max_pages, int n_pages, int page, int32_t* table, int32_t* seq_len, int32_t* refs,
     const int32_t* __restrict__ new_len, int32_t* __restrict__ pairs, int32_t* n_free, int32_t* dev_status) {
@@ -421,7 +422,8 @@ __device__ int check_spans(const CacheGeom& g) {
   return st;
 }
 
-// append: one CTA per (slot, head, touched page), and one that checks
+// append: one CTA per (slot, head, touched page), and one that checks. Bound by memory; the rows' reads go
+// out with the table's entry (behind it, 32 chunks of 513 to 1024 rows took 39 us; now 35, 5.7 TB/s).
 
 constexpr int kAppendThreads = 128;
 
@@ -444,20 +446,39 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(
   const int j = base / g.page + ti;
   const int lo = max(base, j * g.page), hi = min(base + ql, (j + 1) * g.page);   // positions
   if (lo >= hi) return;
-  const int pg = g.table[(size_t)b * g.max_pages + j];
-  if (pg < 0 || pg >= g.n_pages) return;
-  const int vpr = g.d / 8, groups = kAppendThreads / vpr;
+  const int vpr = g.d / 8, groups = kAppendThreads / vpr, n = hi - lo;
   const int vec = threadIdx.x % vpr, row = threadIdx.x / vpr;
   const size_t src = (((size_t)b * g.Hkv + h) * g.T + (lo - base)) * vpr + vec;
+  // (the first rows are on their way with the table's entry)
+  constexpr int U = 4;
+  uint4 a[U], c[U];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * groups;
+      if (r < n) {
+        a[u] = __ldcs(k_new + src + (size_t)r * vpr);
+        c[u] = __ldcs(v_new + src + (size_t)r * vpr);
+      }
+    }
+  };
+  load(row);
+  const int pg = g.table[(size_t)b * g.max_pages + j];
+  if (pg < 0 || pg >= g.n_pages) return;
   const size_t dst = (((size_t)pg * g.Hkv + h) * g.page + (lo - j * g.page)) * vpr + vec;
   Bounds8<F16> bd;
   bd.reset();
-#pragma unroll 4
-  for (int r = row; r < hi - lo; r += groups) {
-    const uint4 a = __ldcs(k_new + src + (size_t)r * vpr), c = __ldcs(v_new + src + (size_t)r * vpr);
-    k[dst + (size_t)r * vpr] = a;
-    v[dst + (size_t)r * vpr] = c;
-    bd.add(a);
+  for (int r0 = row; r0 < n; r0 += U * groups) {
+    if (r0 != row) load(r0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * groups;
+      if (r < n) {
+        k[dst + (size_t)r * vpr] = a[u];
+        v[dst + (size_t)r * vpr] = c[u];
+        bd.add(a[u]);
+      }
+    }
   }
   if (!bounds) return;
   reduce_bounds<F16>(bd, sh, vpr, groups);
