@@ -12,10 +12,12 @@
 //   the score is a product of [min(q,0), max(q,0)] with a page's [kmin, kmax], 2 d long: warp-level MMAs
 //   with fp32 sums, 16 rows (heads x tokens) against 8 pages, the bounds going from global memory
 //   straight into the B fragments (the sum over channels may run in any order, so a lane takes the
-//   channels of its 16-byte loads). One pass over the bounds for up to 16 rows; bound by HBM. Also
-//   the largest magnitude among a page's bounds, for the margin.
-// page_list_kernel: one CTA per (slot, KV head, token). The m-th largest fp32 score theta by radix
-//   selection over keys in shared memory. An MMA sum is off by at most delta = 2^-14 sum|q| max|k|
+//   channels of its 16-byte loads). One pass over the bounds for up to 16 rows; bound by HBM
+//   (10 of its 14 us for 16 users at 64k tokens). Also the largest magnitude among a page's bounds, for the
+//   margin.
+// page_list_kernel: one CTA per (slot, KV head, token), a dozen barriers (11 us there). The m-th largest
+//   score theta: of exact scores by radix selection over keys in shared memory, of the screen's to within
+//   a histogram's bin. An MMA sum is off by at most delta = 2^-14 sum|q| max|k|
 //   (272 additions of at least single precision, 2^-23 each, doubled). At least m pages score
 //   theta - delta or more, so pages below theta - 2 delta are out; pages above theta + 2 delta are in, since
 //   what scores as high as they do lies above theta. Those between (a few) are computed in fp64, a
