@@ -162,3 +162,25 @@ def test_a_list_as_long_as_it_may_be():
     # all of them the same page past the end, the count as large as it may be: all skipped
     out, lse, st = paged.attend_pages(q, cache, torch.full_like(idx, 39), _i32([W, W]).view(2, 1, 1))
     assert int(st) == bb.BSA_DEV_BAD_INDEX and (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("T,Hq,d,dtype", [(1, 4, 128, "bf16"), (2, 8, 128, "fp16"), (1, 3, 64, "fp16"),
+                                          (4, 4, 64, "bf16"), (20, 4, 64, "bf16")])
+def test_one_item_shared_by_every_cta(T, Hq, d, dtype):
+    """One sequence, one KV head: all CTAs leave partial results of one item."""
+    n, page = 90001, 128
+    cache = make_cache(13, lens=[n], max_pages=-(-n // page), page=page, Hkv=1, d=d, dtype=dtype)
+    q = _randn(14, 1, Hq, T, d).to(cache.k.dtype)
+    out, lse, st = paged.attend_tree(q, cache)
+    again, lse2, _ = paged.attend_tree(q, cache)
+    assert int(st) == 0 and torch.equal(out, again) and torch.equal(lse, lse2)
+    see = np.tril(np.ones((T, T), bool))
+    p_bits = 16 if Hq * T <= 16 else 8
+    _check_slot(f8(out[0]), f8(lse[0]), f8(q[0]), cache, 0, n, T, see, dtype, p_bits)
+    # the same as a list of all its pages
+    if T == 1:
+        W = cache.max_pages
+        idx = torch.arange(W, dtype=torch.int32, device="cuda").view(1, 1, 1, W)
+        out, lse, st = paged.attend_pages(q, cache, idx, _i32([W]).view(1, 1, 1))
+        assert int(st) == 0
+        _check_slot(f8(out[0]), f8(lse[0]), f8(q[0]), cache, 0, n, T, see, dtype, 16)
