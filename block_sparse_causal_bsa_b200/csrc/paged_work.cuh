@@ -71,7 +71,8 @@ struct Item {
 };
 
 // How far a share may shrink: below this many tiles per CTA the arrival and the join cost more time
-// than the shorter share saves (one user, eight lists of 64 tiles: 4 tiles 14.6 us, 2 tiles 16.7, 6 tiles 17.3).
+// than the shorter share saves (one user, eight lists of 64 tiles: 4 tiles 14.6 us, 2 tiles 16.7, 6 tiles 17.3;
+// eight drafts over 1003 tokens on tcgen05: 2 tiles 18.8 us, 1 tile 20.9).
 template <int RT>
 constexpr int kMinTiles = RT == 256 ? 2 : 4;
 
