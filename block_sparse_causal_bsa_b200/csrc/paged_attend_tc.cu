@@ -125,6 +125,12 @@ __device__ __forceinline__ uint64_t draft_window(const PagedArgs& a, int b, int 
   return x;
 }
 
+// Of a segment's tiles (the CTA's n-th and up) group g takes the one at this place and, where the groups take turns,
+// every other one after it. At or past the segment's end: the group has no tile there, and its Q is neither
+// brought in nor waited for. (Were q_full counted there too, the softmax warps, held back by the
+// other group alone, could complete it twice before this group's issuer looks once, which then never sees it.)
+__device__ __forceinline__ int first_tile(bool share, int n, int g) { return share ? (n ^ g) & 1 : 0; }
+
 // Parts lie transposed, [D / 4][RT] of four floats: a warp's rows are then neighbours both when a
 // part is written (a thread per row) and when parts are joined.
 __device__ __forceinline__ float4* part4(float* part_o, size_t slot, int D, int d4, int r) {
@@ -280,15 +286,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
     const uint32_t tg = tmem + g * 256;
     const uint64_t descQ = tc::sdesc_sw128(sQ + g * C::kQTile, 16, 1024);
     const uint64_t descK = tc::sdesc_sw128(sK, 16, 1024), descV = tc::sdesc_sw128(sV, C::kHalf, 1024);
-    int n = 0, seg = 0, js = 0, jv = 0;          // tiles of the CTA; products of this group issued
+    int n = 0, nq = 0, js = 0, jv = 0;           // tiles of the CTA; Qs and products of this group
     bool ok = true;
-    for (long long x = x0; ok && x < x1; ++seg) {
+    for (long long x = x0; ok && x < x1;) {
       const long long xe = min(x1, it.first + it.units());
       int ta, tb;
       it.tiles_of(x, xe, ta, tb);
       const int L = tb - ta;
       const bool share = it.rows <= GR;          // the groups take the tiles in turn
-      const int step = share ? 2 : 1, i0 = share ? (n ^ g) & 1 : 0;
+      const int step = share ? 2 : 1, i0 = first_tile(share, n, g);
       int si = i0;                               // the group's next tile of the segment to get its S
       auto next_s = [&]() {
         if (si >= L) return;
@@ -318,8 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
         ++js;
         si += step;
       };
-      ok = warp_all(tc::mbar_wait(&b.q_full, seg & 1, abort_flag, status));
-      if (ok) next_s();
+      if (i0 < L) {
+        ok = warp_all(tc::mbar_wait(&b.q_full, nq & 1, abort_flag, status));
+        ++nq;
+        if (ok) next_s();
+      }
       uint32_t add = 0;
       for (int i = i0; ok && i < L; i += step) {
         const int s = (n + i) % NS;
@@ -396,6 +405,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&b.q_full);
     };
+    // Does the group have a tile in the segment that starts at place x of item i, the CTA's n-th tile?
+    auto has_tile = [&](const Item& i, long long x, int n) {
+      int ta, tb;
+      i.tiles_of(x, min(x1, i.first + i.units()), ta, tb);
+      return first_tile(i.rows <= GR, n, g) < tb - ta;
+    };
     const int my_turn = 4 + 4 * g + quarter, other_turn = 4 + 4 * (1 - g) + quarter;
     if (g == 1) turn_pass(other_turn);
     int n = 0, seg = 0, j = 0;                           // j: tiles of this group
@@ -403,8 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
     Row me{};
     if (x0 < x1) {
       me = row_in(it);
-      load_q(me);
-      q_landed();
+      if (has_tile(it, x0, 0)) {
+        load_q(me);
+        q_landed();
+      }
     }
     for (long long x = x0; x < x1; ++seg) {
       const long long xe = min(x1, it.first + it.units());
@@ -548,10 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
       tc::tc_fence_after();
       // the next item's Q is on its way while this one's result is written
       Item nx = it;
+      bool q_next = false;
       if (xe < x1) {
         w.next(a, nx);
         me = row_in(nx);
-        load_q(me);
+        q_next = has_tile(nx, xe, n);
+        if (q_next) load_q(me);
       }
       const bool whole = x == it.first && xe == it.first + it.units();
       const size_t slot = 2 * (size_t)blockIdx.x + (x == it.first ? 1 : 0);
@@ -617,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
         __syncwarp();
         tc::tc_fence_before();
       }
-      if (xe < x1) q_landed();                           // S of its first tile may start
+      if (q_next) q_landed();                            // S of its first tile may start
       if (!whole) {
         // ---- arrival; the last CTA joins the parts ----
         const int at = share ? 0 : g;
