@@ -131,6 +131,13 @@ __device__ __forceinline__ uint64_t draft_window(const PagedArgs& a, int b, int 
 // other group alone, could complete it twice before this group's issuer looks once, which then never sees it.)
 __device__ __forceinline__ int first_tile(bool share, int n, int g) { return share ? (n ^ g) & 1 : 0; }
 
+// What the state of a row (maximum m, sum l) counts in a join with the maximum mx. An empty state has no weights,
+// l = 0, and counts nothing. Where every score was NaN, m is still -inf (maxima pass NaN by) but l is NaN, which
+// the result has to be, too.
+__device__ __forceinline__ float state_weight(float m, float l, float mx) {
+  return l == 0.f ? 0.f : (l != l ? l : ex2(m - mx));
+}
+
 // Parts lie transposed, [D / 4][RT] of four floats: a warp's rows are then neighbours both when a
 // part is written (a thread per row) and when parts are joined.
 __device__ __forceinline__ float4* part4(float* part_o, size_t slot, int D, int d4, int r) {
@@ -185,8 +192,8 @@ __device__ __noinline__ void join_rows(const PagedArgs& a, const Item& it, const
       }
 #pragma unroll
       for (int k = 0; k < kP; ++k) {
-        const float f = ml[k].x == -INFINITY || i + k >= np ? 0.f : ex2(ml[k].x - mx);
-        if (f == 0.f) continue;                                // (must not meet what an empty part holds)
+        if (i + k >= np || ml[k].y == 0.f) continue;           // (must not meet what an empty part holds)
+        const float f = state_weight(ml[k].x, ml[k].y, mx);
         ls += ml[k].y * f;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
@@ -580,7 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
         if (share) both_sync();
         else group_sync(g);
       };
-      float f0 = first ? 0.f : 1.f, f1 = 0.f;            // weights of the group's state and of the other's
+      float f0 = 1.f, f1 = 0.f;                          // weights of the group's state and of the other's
+      bool some0 = !first, some1 = false;                // ... and whether there is one (else O holds anything)
       if (share) c.ml[g][rt] = make_float2(m_used, l);
       tc::tc_fence_before();
       // the flags and states are there (and no group is more than a segment ahead, whose flags are the
@@ -591,8 +599,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
       if (share) {
         const float2 o = c.ml[1 - g][rt];
         const float m = fmaxf(m_used, o.x);
-        f0 = m_used == -INFINITY ? 0.f : ex2(m_used - m);
-        f1 = o.x == -INFINITY ? 0.f : ex2(o.x - m);
+        f0 = state_weight(m_used, l, m);
+        f1 = state_weight(o.x, o.y, m);
+        some0 = l != 0.f;
+        some1 = o.y != 0.f;
         l = l * f0 + o.y * f1;
         m_used = m;
       }
@@ -606,12 +616,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(
           tc::tmem_ld32(tl + cc * 32, v);
           float y[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = f0 == 0.f ? 0.f : __uint_as_float(v[i]) * (f0 * inv);
+          for (int i = 0; i < 32; ++i) y[i] = some0 ? __uint_as_float(v[i]) * (f0 * inv) : 0.f;
           if (share) {
             tc::tmem_ld32(other + cc * 32, v);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (f1 != 0.f) y[i] = fmaf(__uint_as_float(v[i]), f1 * inv, y[i]);
+              if (some1) y[i] = fmaf(__uint_as_float(v[i]), f1 * inv, y[i]);
           }
           if (row_ok && whole) {
 #pragma unroll
