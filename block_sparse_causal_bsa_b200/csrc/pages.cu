@@ -11,7 +11,7 @@
 //            filled last page that other sequences hold too is replaced by a fresh page (the
 //            (old, new) pair is returned for the copy of its contents, layer by layer)
 //   copy     K, V and bounds of page old -> new
-//   append   rows of new tokens into their pages, and the pages' channel bounds extended
+//   append   rows of new tokens into their pages, and those pages' channel bounds
 //   compact  rows base + keep[i] -> base + i, and the touched pages' bounds recomputed
 //
 // All of them move bytes and compute nothing but minima and maxima: the copies are bound by
@@ -423,7 +423,8 @@ __device__ int check_spans(const CacheGeom& g) {
 }
 
 // append: one CTA per (slot, head, touched page), and one that checks. Bound by memory; the rows' reads go
-// out with the table's entry (behind it, 32 chunks of 513 to 1024 rows took 39 us; now 35, 5.7 TB/s).
+// out with the table's entry (behind it, 32 chunks of 513 to 1024 rows took 39 us; now 37, 5.4 TB/s). The first page's
+// earlier rows are read as well, for its bounds (64 users' rows, replayed: 4.5 us without them, 6.4 with).
 
 constexpr int kAppendThreads = 128;
 
@@ -468,6 +469,17 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(
   const size_t dst = (((size_t)pg * g.Hkv + h) * g.page + (lo - j * g.page)) * vpr + vec;
   Bounds8<F16> bd;
   bd.reset();
+  // The page's rows before the call are read again: the bounds kept with it may be those of more rows, since
+  // dropped by a resize, or of another slot's rows, where the page was copied.
+  const int before = bounds ? lo - j * g.page : 0;
+  const uint4* const old = k + ((size_t)pg * g.Hkv + h) * g.page * vpr + vec;
+  uint4 o[U];                            // (twice as many: 121 registers, 48 drafts compacted 14.6 us for 12.6)
+  auto load_old = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r0 + u * groups < before) o[u] = old[(size_t)(r0 + u * groups) * vpr];
+  };
+  load_old(row);                         // (on their way while the new rows are written)
   for (int r0 = row; r0 < n; r0 += U * groups) {
     if (r0 != row) load(r0);
 #pragma unroll
@@ -480,11 +492,16 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(
       }
     }
   }
+  for (int r0 = row; r0 < before; r0 += U * groups) {
+    if (r0 != row) load_old(r0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r0 + u * groups < before) bd.add(o[u]);
+  }
   if (!bounds) return;
   reduce_bounds<F16>(bd, sh, vpr, groups);
   if ((int)threadIdx.x < vpr) {
     uint4* bp = bounds + ((size_t)pg * g.Hkv + h) * 2 * vpr + threadIdx.x;
-    if (lo > j * g.page) bd.merge(bp[0], bp[vpr]);     // rows before the call stay covered
     bp[0] = bd.vlo();
     bp[vpr] = bd.vhi();
   }

@@ -9,7 +9,7 @@ A step, for the sequences ("slots") of a :class:`PagedCache`::
         out, lse, st = paged.attend_tree(q, cache, mask=mask, q_len=q_len, layer=layer)
         # or: sel = paged.select_pages(q, cache, cfg, q_len=q_len, layer=layer)
         #     out, lse, st = paged.attend_pages(q, cache, sel["kv_idx"], sel["kv_cnt"], ...)
-    # after the drafts are verified, per layer:
+    # after the drafts are verified, per layer (a chain of which the first ones are accepted needs none):
         paged.compact(cache, keep, n_keep, q_len=q_len, layer=layer)
     paged.resize(cache, cache.seq_len - q_len + n_keep)   # the rejected drafts' pages
 
@@ -253,7 +253,7 @@ def copy_pages(cache: PagedCache, pairs: torch.Tensor, *, layer: int = 0, stream
 def append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, *, q_len=None, layer: int = 0,
            stream=None) -> torch.Tensor:
     """Writes k_new, v_new [slots, Hkv, T, d] to the last q_len positions of the slots (resize
-    comes first) and extends their pages' bounds. Returns the status."""
+    comes first) and sets their pages' bounds. Returns the status."""
     p = cache._plan or cache._make_plan()
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
         _bad("k_new must be [slots, Hkv, T, d]")

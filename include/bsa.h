@@ -379,6 +379,9 @@ bsa_status bsa_pages_fork(int slots, int max_pages, int n_pages, int page, int32
  * for the page that holds their last rows if other slots hold it too (the slot gets a page of its own, and
  * pairs[s] = (old, new) for bsa_pages_copy), then the pages of their new positions. When all
  * holders of such a shared page grow in one call, the last of them keeps it.
+ * The bounds are not its business: a slot that shrinks into a page keeps that page's bounds over the dropped
+ * rows as well until its next append or compact. That page is the slot's last, which every
+ * selection keeps unranked; its score, where scores are asked for, is an upper bound until then.
  * If there are not enough free pages, the slots (in slot order) from the first that does not fit on
  * keep their length if they need any (BSA_DEV_NO_PAGES).
  *   pairs  [slots,2] int32: (-1,-1) where nothing is to be copied. Copy every layer before the
@@ -397,8 +400,8 @@ bsa_status bsa_pages_copy(const bsa_cache_shape* shape, void* k_pages, void* v_p
                           const int32_t* pairs, int n_pairs, int32_t* dev_status, void* stream);
 
 /* Append: writes k_new, v_new [slots,Hkv,T,d] to the positions of the call's tokens (seq_len
- * already counts them: resize comes first) and extends the bounds (NULL: none) of the pages they
- * fall in; a page whose first row is among them starts afresh. A page that is written must not
+ * already counts them: resize comes first) and sets the bounds (NULL: none) of the pages they
+ * fall in to those of the pages' rows up to the last of them. A page that is written must not
  * be held by another slot, which would see the change (a resize that grows the slot gives it
  * a page of its own). */
 bsa_status bsa_cache_append(const bsa_cache_shape* shape, int slots, int max_pages, int T,
