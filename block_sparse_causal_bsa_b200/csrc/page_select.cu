@@ -566,8 +566,7 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
       st |= u == kNoPage ? BSA_DEV_BAD_INDEX : BSA_DEV_BAD_SCORE;
       key = 0;                                  // ranks last
     } else if (SCREEN) {
-      // an estimate that is not finite (an overflow, a query that is not finite) says nothing: an
-      // infinite margin has every page computed
+      // (where an estimate is not finite, none is used: see the margin below)
       const bool over = !(fabsf(v) < INFINITY);
       kabs = fmaxf(kabs, over ? INFINITY : __uint_as_float(u));
       if (over) key = 1;
@@ -634,10 +633,14 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
     __syncthreads();
     const unsigned klo = mn + (s.digit << sh), khi = klo + ((1u << sh) - 1u);
     const float th_lo = key_score(klo), th_hi = key_score(min(khi, mx));
+    // Below 2^127 no sum of the screen overflows, in any head, and estimates are off by delta at most. Above (or with a
+    // query that is not finite) they say nothing: every page that is not known to be bad is computed, and ranked with
+    // those that are.
+    const float span = q1 * kabs;
+    const bool usable = span < 0x1p127f;
     // 2^-14 for the sums; what 16-bit subnormals could lose if an MMA flushed them
-    const float delta = 0x1p-14f * q1 * kabs + (F16 ? 0x1p-13f : 0x1p-100f) * (q1 + g.d * kabs);
-    const float lo = th_lo - 2.f * delta, hi = th_hi + 2.f * delta;
-    // (an infinite or NaN margin puts everything but the pages known to be bad, key 0, in the window)
+    const float delta = 0x1p-14f * span + (F16 ? 0x1p-13f : 0x1p-100f) * (q1 + g.d * kabs);
+    const float lo = usable ? th_lo - 2.f * delta : -INFINITY, hi = usable ? th_hi + 2.f * delta : INFINITY;
     const unsigned sure = hi < INFINITY ? score_key(hi) : 0xfffffffeu;      // keys above it are in
     int in = 0;
     for (int i = tid; i < n; i += kListThreads) {
@@ -658,9 +661,9 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
     const int32_t* table = g.table + (size_t)b * g.max_pages + p.n_first;
     const uint16_t* bh_bounds = bounds + (size_t)h * 2 * g.d;
     const size_t page_stride = (size_t)g.Hkv * 2 * g.d;
-    if (nw < need) {
+    if (usable && nw < need) {
       c = Cut{0u, 0xffffffffu, need - nw};       // every page that is not bad, and the first bad ones
-    } else if (nw <= kWindow) {
+    } else if (usable && nw <= kWindow) {
       c = Cut{sure, 0xffffffffu, 0};
       if (nw > need) {
         // exact scores of the window, a warp per page, then ranks within it
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
         if (better < need) keys[i] = 0xffffffffu;
       }
     } else {
-      // a large window (copies of pages, an unusable margin): its exact keys, and another selection
+      // a large window (copies of pages), or estimates that say nothing: exact keys, and another selection
       for (int i = warp; i < n; i += kListWarps) {
         const unsigned key = keys[i];
         unsigned exact = key > sure ? 0xffffffffu : 0u;
