@@ -356,7 +356,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_screen_kernel(
       float m;
       if (F16) asm("cvt.f32.f16 %0, %1;" : "=f"(m) : "h"((uint16_t)mx));
       else m = __uint_as_float(mx << 16);
-      kmax_abs[(size_t)bh * g.max_pages + jw + g8] = held ? m : __uint_as_float(kNoPage);
+      // (a NaN that was converted may have any bits, those of kNoPage too)
+      kmax_abs[(size_t)bh * g.max_pages + jw + g8] =
+          __uint_as_float(!held ? kNoPage : m < INFINITY ? __float_as_uint(m) : kBadScore);
     }
     // rows g8 (r[0], r[1]) and g8 + 8 (r[2], r[3]) of pages jw + 2 tig (+1): maximum over the heads
     float r[4];

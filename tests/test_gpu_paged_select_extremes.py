@@ -134,3 +134,14 @@ def test_magnitudes_over_the_whole_range(dtype, span, G, d):
         if seed == 5:
             cache.page_table[0, 50] = -1
         _check(q, cache, paged.PageSelectConfig([9, 60, 150][seed % 3], 1, 2), (dtype, span, seed))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("val", [float("nan"), float("inf"), float("-inf")])
+def test_bounds_that_are_not_finite_are_bad_scores(dtype, val):
+    """... and not pages that the table lacks."""
+    for chan in (0, 9, 63):
+        cache = _cache(dtype)
+        pg = cache.page_table[0, 12].item()
+        cache.bounds[0, pg, 0, 1, chan] = val
+        _check(_q(2, dtype=dtype), cache, paged.PageSelectConfig(8, 1, 1), (dtype, val, chan))
