@@ -17,8 +17,9 @@
 //   margin.
 // page_list_kernel: one CTA per (slot, KV head, token), a dozen barriers (11 us there). The m-th largest
 //   score theta: of exact scores by radix selection over keys in shared memory, of the screen's to within
-//   a histogram's bin. An MMA sum is off by at most delta = 2^-14 sum|q| max|k|
-//   (272 additions of at least single precision, 2^-23 each, doubled). At least m pages score
+//   a few delta by one or two histograms. An MMA sum is off by at most delta = 2^-14 sum|q| max|k|: 273
+//   additions and roundings of 2^-23 each, at least single precision's, come to 2^-14.9; the rest covers the roundings of
+//   sum|q|, of theta +- 2 delta and of the exact score to fp32. At least m pages score
 //   theta - delta or more, so pages below theta - 2 delta are out; pages above theta + 2 delta are in, since
 //   what scores as high as they do lies above theta. Those between (a few) are computed in fp64, a
 //   warp per page, and ranked by (fp32 rounding desc, index asc).
@@ -574,8 +575,10 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
       if (over) key = 1;
     }
     keys[i] = key;
-    mn = min(mn, key);
-    mx = max(mx, key);
+    if (!SCREEN || key > 1) {                   // (bad pages take no part in the range of the screen's scores)
+      mn = min(mn, key);
+      mx = max(mx, key);
+    }
   }
   if (st) atomicOr(&s.status, st);
   mn = __reduce_min_sync(0xffffffffu, mn);
@@ -605,36 +608,6 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
   if (!SCREEN) c = radix_cut(keys, n, m, mn, mx, s);
 
   if (SCREEN) {
-    // the threshold to within 2^-11 of the keys' range, which the margin exceeds: one histogram of equal
-    // ranges of keys
-    const int sh = max(0, 21 - __clz(mx - mn | 1u));
-    for (int i = tid; i < n; i += kListThreads) atomicAdd(&s.hist[(keys[i] - mn) >> sh], 1u);
-    __syncthreads();
-    // thread tid: the bins 4 d .. 4 d + 3 and the keys above them, from the top down
-    const int d = kBins / 4 - 1 - tid;
-    const uint4 h4 = *reinterpret_cast<const uint4*>(&s.hist[4 * d]);
-    const unsigned mine = h4.x + h4.y + h4.z + h4.w;
-    unsigned x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s.red[warp] = x;
-    __syncthreads();
-    unsigned above = x - mine;
-    for (int i = 0; i < warp; ++i) above += s.red[i];
-    const unsigned um = (unsigned)m;
-    if (above < um && above + mine >= um) {
-      unsigned at = above, bin = 4 * d + 3;
-      if (at + h4.w < um) { at += h4.w; --bin;
-        if (at + h4.z < um) { at += h4.z; --bin;
-          if (at + h4.y < um) { at += h4.y; --bin; } } }
-      s.digit = bin;
-    }
-    __syncthreads();
-    const unsigned klo = mn + (s.digit << sh), khi = klo + ((1u << sh) - 1u);
-    const float th_lo = key_score(klo), th_hi = key_score(min(khi, mx));
     // Below 2^127 no sum of the screen overflows, in any head, and estimates are off by delta at most. Above (or with a
     // query that is not finite) they say nothing: every page that is not known to be bad is computed, and ranked with
     // those that are.
@@ -642,6 +615,57 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
     const bool usable = span < 0x1p127f;
     // 2^-14 for the sums; what 16-bit subnormals could lose if an MMA flushed them
     const float delta = 0x1p-14f * span + (F16 ? 0x1p-13f : 0x1p-100f) * (q1 + g.d * kabs);
+    // The threshold, to within a few delta: a histogram of equal ranges of the finite scores' keys. Where a bin is wider
+    // (scores of both signs: their keys lie far apart) a second one of its keys; a bin of that is at most 2^10 keys,
+    // 2^-13 of its scores, that is 2 delta. (One histogram over all keys, bad pages' among them, left windows of hundreds of
+    // pages: selection at 128k tokens with one page missing 420 us, now 16; sixteen users at 64k with scores around zero
+    // 37, now 25.)
+    unsigned klo = mn, khi = mx, rank = (unsigned)m, finite = 0;
+    float th_lo = 0.f, th_hi = 0.f;
+    for (int level = 0; usable; ++level) {
+      const int sh = max(0, 21 - __clz((khi - klo) | 1u));
+#pragma unroll 4
+      for (int i = tid; i < n; i += kListThreads) {
+        const unsigned key = keys[i];
+        if (key - klo <= khi - klo) atomicAdd(&s.hist[(key - klo) >> sh], 1u);
+      }
+      __syncthreads();
+      // thread tid: the bins 4 d .. 4 d + 3 and the keys above them, from the top down
+      const int d = kBins / 4 - 1 - tid;
+      const uint4 h4 = *reinterpret_cast<const uint4*>(&s.hist[4 * d]);
+      const unsigned mine = h4.x + h4.y + h4.z + h4.w;
+      unsigned x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) s.red[warp] = x;
+      __syncthreads();
+      const unsigned part = lane < kListWarps ? s.red[lane] : 0u;
+      const unsigned above = x - mine + __reduce_add_sync(0xffffffffu, lane < warp ? part : 0u);
+      const unsigned all = __reduce_add_sync(0xffffffffu, part);
+      if (level == 0) finite = all;
+      if (all < rank) break;                    // fewer finite scores than places
+      if (above < rank && above + mine >= rank) {
+        unsigned at = above, bin = 4 * d + 3;
+        if (at + h4.w < rank) { at += h4.w; --bin;
+          if (at + h4.z < rank) { at += h4.z; --bin;
+            if (at + h4.y < rank) { at += h4.y; --bin; } } }
+        s.digit = bin;
+        s.above = at;
+      }
+      __syncthreads();
+      klo += s.digit << sh;
+      khi = min(khi, klo + ((1u << sh) - 1u));
+      rank -= s.above;
+      th_lo = key_score(klo);
+      th_hi = key_score(khi);
+      if (level || !(th_hi - th_lo > 8.f * delta)) break;
+      *reinterpret_cast<uint4*>(&s.hist[4 * d]) = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+    }
+    const bool few = finite < (unsigned)m;
     const float lo = usable ? th_lo - 2.f * delta : -INFINITY, hi = usable ? th_hi + 2.f * delta : INFINITY;
     const unsigned sure = hi < INFINITY ? score_key(hi) : 0xfffffffeu;      // keys above it are in
     int in = 0;
@@ -663,8 +687,8 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(
     const int32_t* table = g.table + (size_t)b * g.max_pages + p.n_first;
     const uint16_t* bh_bounds = bounds + (size_t)h * 2 * g.d;
     const size_t page_stride = (size_t)g.Hkv * 2 * g.d;
-    if (usable && nw < need) {
-      c = Cut{0u, 0xffffffffu, need - nw};       // every page that is not bad, and the first bad ones
+    if (usable && few) {
+      c = Cut{0u, 0xffffffffu, m - (int)finite};   // every page that is not bad, and the first bad ones
     } else if (usable && nw <= kWindow) {
       c = Cut{sure, 0xffffffffu, 0};
       if (nw > need) {

@@ -145,3 +145,21 @@ def test_bounds_that_are_not_finite_are_bad_scores(dtype, val):
         pg = cache.page_table[0, 12].item()
         cache.bounds[0, pg, 0, 1, chan] = val
         _check(_q(2, dtype=dtype), cache, paged.PageSelectConfig(8, 1, 1), (dtype, val, chan))
+
+
+@pytest.mark.parametrize("k", [5, 64, 300])
+@pytest.mark.parametrize("G,d,dtype", [(4, 128, "bf16"), (2, 64, "fp16"), (16, 64, "bf16")])
+@pytest.mark.parametrize("lean", [0.0, 0.4, 0.7, 1.0])
+def test_scores_of_both_signs(k, G, d, dtype, lean):
+    """Keys with channel offsets and a query against them: scores around zero, where few or many 32-bit keys lie
+    between two pages; with pages missing, too."""
+    pages = 700
+    cache = _cache(dtype, d, pages=pages, seed=int(10 * lean) + G)
+    off = 3 * torch.sign(torch.randn(d, generator=torch.Generator().manual_seed(d)))
+    cache.bounds += off.to(DT[dtype]).cuda()
+    q = (_q(G, d, k, dtype).float() - lean * off).to(DT[dtype])
+    cfg = paged.PageSelectConfig(k, 1, 2)
+    _check(q, cache, cfg, (lean, k))
+    for j in (0, 17, 400, 699):
+        cache.page_table[0, j] = -1
+    _check(q, cache, cfg, (lean, k, "missing"))
