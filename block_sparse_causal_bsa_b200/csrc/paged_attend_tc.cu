@@ -27,8 +27,9 @@
 // (its error against 64 bits, random values in bf16: 0.0021 relative rms, where rounding the exact output alone
 // gives 0.0017); sums and maxima are fp32. For fp16, weights carry a factor 2^7: with the maximum up to 2^8
 // stale they stay below 2^15, and weights down to 2^-31 of the largest still count.
-// Measured: 8 users with 64 drafts (256 rows per KV head) over 32768 tokens, 300 us, 916 TFLOP/s; 24 users with 9
-// to 33 drafts, d = 64, 93 us. Of the 2070 cycles of a tile of 256 rows, its products take 1270 when nothing
+// Measured: 8 users with 64 drafts (256 rows per KV head) over 32768 tokens, 300 us, 916 TFLOP/s, in a few dozen replays
+// at 1965 MHz; from half a second on the 1000 W limit leaves 1545 MHz, 345 to 355 us. 24 users with 9 to 33 drafts, d = 64:
+// 92 us (1965 MHz throughout). Of the 2070 cycles of a tile of 256 rows, its products take 1270 when nothing
 // else runs (S of 64 columns is bound by the reads of Q from shared memory, 418 cycles for 256 of
 // products) and its exponentials 1024. Tried: S of 128 keys at once (one buffer then, or two rewritten
 // together, so that S cannot run ahead of the value products: 462 and 369 us), two threads per row (850 us:

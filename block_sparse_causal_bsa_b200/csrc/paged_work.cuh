@@ -363,7 +363,15 @@ cudaError_t launch_paged_attend_tc(const bsa_cache_shape& s, const PagedArgs& a,
 // Shares per SM of the kernel on warp-level MMAs: the CTAs that fit.
 constexpr int kMmaSharesPerSm = 2;
 
-// Query rows per KV head up to which a call runs on warp-level MMAs.
+// Query rows per KV head up to which a call runs on warp-level MMAs (of the call's T: lengths are on the device).
+// Both kernels at 8 KV heads, bf16, graph replays in us, warp-level MMAs against tcgen05 (above 16 rows the former
+// takes 16 at a time):
+//                              4 rows      8 rows      16 rows     20 rows      32 rows      64 rows
+//   d 128, 1 x 1000 tokens     14 : 18     17 : 18     21 : 19     22 : 19      23 : 18      24 : 21
+//   d 128, 1 x 64000           58 : 68     63 : 69     81 : 69     91 : 69     101 : 68     183 : 74
+//   d 128, 16 x 64000         613 : 616   616 : 688   640 : 677  1260 : 620   1242 : 692   2454 : 755
+//   d 64, 1 x 64000            43 : 71     44 : 65     51 : 61     66 : 62      68 : 60     104 : 60
+//   d 64, 16 x 64000          327 : 552   328 : 552   325 : 552   624 : 579    677 : 555   1329 : 552
 constexpr int kMaxMmaRows = 16;
 
 }  // namespace bsa

@@ -435,6 +435,10 @@ bsa_status bsa_tree_mask(int B, int T, const int32_t* parents, const int32_t* q_
  *   [slots,Hq,T] fp32 or NULL, the natural log of the softmax denominator. A token that sees nothing
  *   gets 0 and -inf. K and V rows that a token does not see do not touch its result, whatever they
  *   hold (NaN and infinities included).
+ *   Softmax statistics and sums are fp32. Up to 16 query rows per KV head (Hq/Hkv * T) the weights enter the
+ *   value product with twice the type's bits, from 17 on rounded to the type (bf16 2^-8, fp16 2^-11
+ *   each): random values' outputs are then off by 0.0021 to 0.0023 (bf16, relative rms) instead of 0.0017.
+ *   A NaN score of a position seen makes the token's result NaN.
  *   Hq a multiple of Hkv, Hq/Hkv <= 16. The workspace (bsa_attend_paged_workspace_bytes, 256-byte
  *   aligned) need not be initialised; concurrent calls need one each. */
 bsa_status bsa_attend_tree(const bsa_cache_shape* shape, int slots, int max_pages, int Hq, int T,
