@@ -15,7 +15,9 @@ A step, for the sequences ("slots") of a :class:`PagedCache`::
 
 The calls run on the current stream of the cache's device (or on ``stream``) and return at once.
 Arguments that the host can check raise :class:`BsaError`; what only the device sees is in the
-status tensors returned. ``include/bsa.h`` ("paged cache") says what each call does.
+status tensors returned. ``include/bsa.h`` ("paged cache") says what each call does. Output rows of
+tokens that a call leaves out (past q_len, or of a slot whose lengths do not fit) are not written: in tensors
+made here they are 0 (lse: -inf) when q_len is given, and undefined when it is not.
 """
 from __future__ import annotations
 
